@@ -15,11 +15,29 @@ from . import build as _build
 _lock = threading.Lock()
 _lib = None
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_ALIGNMENT, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(6)
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_ALIGNMENT, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_INDEX = range(7)
+
+FA_CACHE_BF16, FA_CACHE_E4M3 = range(2)
+
+
+class CacheStruct(ctypes.Structure):
+    """fa_paged_cache"""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("K_scale", ctypes.c_void_p),
+                ("V_scale", ctypes.c_void_p), ("type", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("heads", ctypes.c_int), ("page_size", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class BatchStruct(ctypes.Structure):
+    """fa_paged_batch"""
+    _fields_ = [("block_table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("max_pages", ctypes.c_int), ("max_q", ctypes.c_int)]
+
 
 # Every entry point declared in include/fa.h: name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_CACHE, _BATCH = ctypes.POINTER(CacheStruct), ctypes.POINTER(BatchStruct)
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _I, _P]),
     "fa_bwd_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I]),
@@ -38,6 +56,9 @@ SIGNATURES = {
     "fa_accumulate_bf16": (_I, [_P, _P, ctypes.c_int64, _I, _P]),
     "fa_accumulate_f32": (_I, [_P, _P, ctypes.c_int64, _P]),
     "fa_convert_f32_bf16": (_I, [_P, _P, ctypes.c_int64, _P]),
+    "fa_cache_append": (_I, [_CACHE, _BATCH, _I, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _P]),
+    "fa_fwd_paged_workspace_size": (ctypes.c_size_t, [_CACHE, _BATCH, _I, _I]),
+    "fa_fwd_paged": (_I, [_P, _L, _CACHE, _BATCH, _I, _P, _P, _P, ctypes.c_size_t, _I, ctypes.c_float, _I, _P]),
     "fa_strerror": (ctypes.c_char_p, [_I]),
     "fa_last_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_int)]),
     "fa_set_softmax_options": (_I, [ctypes.c_float, _I]),

@@ -6,6 +6,7 @@ computation runs in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -15,6 +16,7 @@ from . import _lib
 from ._lib import check
 
 _BF16 = torch.bfloat16
+_E4M3 = torch.float8_e4m3fn
 
 
 def _ptr(t: torch.Tensor | None):
@@ -229,6 +231,162 @@ def fa_bwd_finish(workspace, B: int, Hq: int, Nq: int, d: int, scale: float | No
     check(_lib.lib().fa_bwd_finish(_ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), B, Hq,
                                    Nq, d, scale, _stream(stream)), "fa_bwd_finish")
     return out
+
+
+class PagedCache:
+    """A paged key/value cache: k_pages, v_pages [num_pages, Hkv, page_size, d], bf16, or float8_e4m3fn
+    with k_scale, v_scale fp32 [num_pages, Hkv] (a held value stands for code * scale).  page_size 16,
+    32, 64 or 128; d 64 or 128.  Holds the tensors and describes them to the library; the caller hands
+    out the pages."""
+
+    def __init__(self, k_pages, v_pages, k_scale=None, v_scale=None):
+        if k_pages.dim() != 4:
+            raise ValueError("expected [num_pages, Hkv, page_size, d] pages")
+        pages, heads, size, d = (int(x) for x in k_pages.shape)
+        if k_pages.dtype not in (_BF16, _E4M3):
+            raise ValueError(f"k_pages: expected {_BF16} or {_E4M3}, got {k_pages.dtype}")
+        if size not in (16, 32, 64, 128) or d not in (64, 128):
+            raise ValueError(f"page_size {size}, d {d}: expected page_size 16, 32, 64 or 128 and d 64 or 128")
+        fp8 = k_pages.dtype == _E4M3
+        for t, nm in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            _need(t, nm, k_pages.dtype, (pages, heads, size, d))
+        if (k_scale is None) == fp8 or (v_scale is None) == fp8:
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn pages, both of them")
+        if fp8:
+            for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _need(t, nm, torch.float32, (pages, heads))
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.d = pages, heads, size, d
+        self.device = k_pages.device
+        self._c = _lib.CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr() if fp8 else None,
+                                   v_scale.data_ptr() if fp8 else None,
+                                   _lib.FA_CACHE_E4M3 if fp8 else _lib.FA_CACHE_BF16, pages, heads, size, d)
+        self._ref = ctypes.byref(self._c)
+
+
+class PagedBatch:
+    """B sequences of a paged cache: block_table int32 [B, max_pages], cu_q int32 [B + 1] (the token rows
+    of each), seq_lens int32 [B] (tokens in all, the new ones last), max_q (no sequence has more new
+    tokens).  The tensors are read when the kernels run: refill them in place from step to step."""
+
+    def __init__(self, block_table, cu_q, seq_lens, max_q: int):
+        if block_table.dim() != 2:
+            raise ValueError("block_table: expected [B, max_pages]")
+        B, max_pages = (int(x) for x in block_table.shape)
+        _need(block_table, "block_table", torch.int32, (B, max_pages))
+        _need(cu_q, "cu_q", torch.int32, (B + 1,))
+        _need(seq_lens, "seq_lens", torch.int32, (B,))
+        if int(max_q) < 0:
+            raise ValueError("max_q must not be negative")
+        self.block_table, self.cu_q, self.seq_lens = block_table, cu_q, seq_lens
+        self.B, self.max_pages, self.max_q = B, max_pages, int(max_q)
+        self.device = block_table.device
+        self._c = _lib.BatchStruct(block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), B, max_pages,
+                                   self.max_q)
+        self._ref = ctypes.byref(self._c)
+
+
+def _need_rows(t: torch.Tensor, name: str, heads: int, d: int, rows: int | None = None) -> int:
+    """Checks token-major rows [T, heads, d] with each row contiguous; returns the elements between rows."""
+    if t.dtype != _BF16 or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (
+            rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: expected CUDA {_BF16} [{'T' if rows is None else rows}, {heads}, {d}], got "
+                         f"{t.dtype} {tuple(t.shape)} cuda={t.is_cuda}")
+    if t.shape[0] == 0 or heads == 0:
+        return heads * d
+    row, head, col = t.stride()
+    if col != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{name}: expected each token's {heads} x {d} elements contiguous, got strides {t.stride()}")
+    _on_current_device(t, name)
+    return row if t.shape[0] > 1 else max(row, heads * d) // 8 * 8
+
+
+def _on_stream(stream):
+    """The context in which to allocate for a call on `stream` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
+
+
+def _same_device(cache: PagedCache, batch: PagedBatch):
+    cur = torch.cuda.current_device()
+    for x, name in ((cache, "cache"), (batch, "batch")):
+        if x.device.index != cur:
+            raise ValueError(f"{name}: on {x.device}, but the current device is cuda:{cur}")
+
+
+def fa_cache_append(k, v, cache: PagedCache, batch: PagedBatch, cos=None, sin=None, interleaved: bool = False,
+                    q=None, q_out=None, stream=None):
+    """Append the new tokens' k, v (bf16 [T, Hkv, d]; rows may be strided, as slices of a fused projection)
+    to the cache.  cos, sin fp32 [positions, rot / 2] rotate the keys, and the queries q (bf16 [T, Hq, d])
+    into q_out (new, given, or q itself), by the tokens' positions: pairs (i, i + rot/2), or (2i, 2i + 1)
+    when interleaved.  Returns the rotated queries (None without q)."""
+    T = int(k.shape[0])
+    ldk = _need_rows(k, "k", cache.heads, cache.d)
+    ldv = _need_rows(v, "v", cache.heads, cache.d, T)
+    _same_device(cache, batch)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin belong together")
+    rot = n_pos = 0
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos: expected [positions, rot / 2]")
+        n_pos, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
+        if rot == 0 or rot > cache.d or rot % 16:
+            raise ValueError(f"cos, sin turn {rot} of {cache.d} columns: expected a multiple of 16, at most {cache.d}")
+        _need(cos, "cos", torch.float32, (n_pos, rot // 2))
+        _need(sin, "sin", torch.float32, (n_pos, rot // 2))
+    ldq = ldqo = Hq = 0
+    if q is not None:
+        if rot == 0:
+            raise ValueError("q is given to be rotated: it needs cos and sin")
+        Hq = int(q.shape[1]) if q.dim() == 3 else -1
+        ldq = _need_rows(q, "q", Hq, cache.d, T)
+        if cache.heads == 0 or Hq % cache.heads:
+            raise ValueError(f"q: {Hq} heads over {cache.heads} key/value heads")
+        if q_out is None:
+            with _on_stream(stream):
+                q_out = torch.empty((T, Hq, cache.d), dtype=_BF16, device=q.device)
+        ldqo = _need_rows(q_out, "q_out", Hq, cache.d, T)
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    check(_lib.lib().fa_cache_append(cache._ref, batch._ref, T, _ptr(k), ldk, _ptr(v), ldv, _ptr(q), ldq,
+                                     _ptr(q_out), ldqo, Hq, _ptr(cos), _ptr(sin), rot, int(bool(interleaved)),
+                                     n_pos, _stream(stream)), "fa_cache_append")
+    return q_out
+
+
+def fa_fwd_paged_workspace_size(cache: PagedCache, batch: PagedBatch, T: int, Hq: int) -> int:
+    return int(_lib.lib().fa_fwd_paged_workspace_size(cache._ref, batch._ref, T, Hq))
+
+
+def fa_fwd_paged(q, cache: PagedCache, batch: PagedBatch, scale: float | None = None, causal: bool = True,
+                 out=None, lse=None, workspace=None, stream=None):
+    """O [T, Hq, d], LSE [T, Hq] of the new tokens' queries q (bf16 [T, Hq, d]; rows may be strided) over
+    their sequences in the cache: single tokens, a few, prompt chunks, or a mixture.  causal: token i of
+    n new ones sees its sequence's keys but the last n - 1 - i.  A row that sees no key gets O = 0,
+    LSE = -inf; rows behind the batch's last are left as they were."""
+    T, Hq = int(q.shape[0]), int(q.shape[1]) if q.dim() == 3 else -1
+    ldq = _need_rows(q, "q", Hq, cache.d)
+    if cache.heads == 0 or Hq % cache.heads:
+        raise ValueError(f"q: {Hq} heads over {cache.heads} key/value heads")
+    _same_device(cache, batch)
+    scale = 1.0 / math.sqrt(cache.d) if scale is None else float(scale)
+    ws_bytes = fa_fwd_paged_workspace_size(cache, batch, T, Hq)
+    if out is None or lse is None or workspace is None:
+        with _on_stream(stream):
+            out = torch.empty((T, Hq, cache.d), dtype=_BF16, device=q.device) if out is None else out
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+            if workspace is None:
+                workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+    _need(out, "out", _BF16, (T, Hq, cache.d))
+    _need(lse, "lse", torch.float32, (T, Hq))
+    _need_workspace(workspace, ws_bytes)
+    check(_lib.lib().fa_fwd_paged(_ptr(q), ldq, cache._ref, batch._ref, T, _ptr(out), _ptr(lse), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), Hq, scale, int(bool(causal)),
+                                  _stream(stream)), "fa_fwd_paged")
+    return out, lse
 
 
 def fa_lse_merge(o_part, lse_part, o_acc, lse_acc, first: bool = False, stream=None) -> None:

@@ -23,11 +23,11 @@ def nvcc() -> str:
 
 
 def _sources():
-    return [os.path.join(CSRC, "fa_api.cu")]
+    return [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_paged_api.cu")]
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "fa.h")]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "fa.h")]
 
 
 def up_to_date(out: str = LIB) -> bool:
@@ -39,7 +39,7 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
         return out
     os.makedirs(os.path.dirname(out), exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "--threads", "0",
            "-I", os.path.join(ROOT, "include"), *extra, "-o", tmp, *_sources()]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

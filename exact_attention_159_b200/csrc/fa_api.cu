@@ -16,11 +16,14 @@
 #include "fa_bwd2.cuh"
 #include "fa_fwd.cuh"
 #include "fa_fwd2.cuh"
+#include "fa_host.h"
 #include "fa_merge.cuh"
+#include "fa_paged.cuh"
+
+using namespace fa_host;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 // Forward: element pairs out of every 16 whose exponentials take the FMA-pipe cubic by default,
 // per head dimension (index 0: d = 64, 1: d = 128).
 constexpr int kPolyDefault[2] = {4, 1};
@@ -56,6 +59,10 @@ void prof_end(int which, cudaStream_t st) {
   g_prof[which][0] = g_prof[which][1] = nullptr;
 }
 
+}  // namespace
+
+namespace fa_host {
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -87,24 +94,6 @@ int* device_status(int* err_out) {
   return s.status;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-// Encoded tensor maps of recent calls, keyed by (address, extents, box, element kind): callers that
-// reuse their buffers (training loops, graph replays, the ring steps) skip cuTensorMapEncodeTiled.
-// A map holds only the address and geometry it was encoded from, so a hit is exactly the map a
-// fresh encode would produce.  Small, round-robin replacement, one lock.
-struct MapKey {
-  const void* base;
-  int BH, N, d, rows, kind;  // kind 0: bf16 operand, 1: fp32 dQ accumulator
-  bool operator==(const MapKey& o) const {
-    return base == o.base && BH == o.BH && N == o.N && d == o.d && rows == o.rows && kind == o.kind;
-  }
-};
 struct MapCache {
   static constexpr int kSlots = 64;
   std::mutex mu;
@@ -112,7 +101,7 @@ struct MapCache {
   CUtensorMap map[kSlots];
   int used = 0, next = 0;
 };
-MapCache g_maps;
+static MapCache g_maps;
 
 bool map_lookup(const MapKey& k, CUtensorMap* out) {
   std::lock_guard<std::mutex> lock(g_maps.mu);
@@ -130,6 +119,32 @@ void map_store(const MapKey& k, const CUtensorMap& m) {
   g_maps.key[i] = k;
   g_maps.map[i] = m;
 }
+
+// The dynamic shared memory limit of a kernel is a per-device attribute: set it once per (kernel,
+// device) and remember that it is set.
+static std::mutex g_attr_mu;
+struct AttrDone {
+  const void* kernel;
+  int device;
+};
+static AttrDone g_attr_done[256];
+static int g_attr_count = 0;
+
+cudaError_t set_smem_limit(const void* key, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_attr_mu);
+  for (int i = 0; i < g_attr_count; ++i)
+    if (g_attr_done[i].kernel == key && g_attr_done[i].device == dev) return cudaSuccess;
+  e = cudaFuncSetAttribute(key, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && g_attr_count < 256) g_attr_done[g_attr_count++] = AttrDone{key, dev};
+  return e;
+}
+
+}  // namespace fa_host
+
+namespace {
 
 // 3-D map over a contiguous [BH, N, d] bf16 tensor: box 64 (d) x `rows` x 1, 128-byte swizzle.
 bool make_map(CUtensorMap* map, const void* base, int BH, int N, int d, int rows = 128) {
@@ -192,30 +207,6 @@ int check_shape(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int 
   }
   if (static_cast<long long>(B) * Hq * ((Nq + 127) / 128) > INT_MAX) return FA_ERR_UNSUPPORTED;
   return FA_OK;
-}
-
-// The dynamic shared memory limit of a kernel is a per-device attribute: set it once per (kernel,
-// device) and remember that it is set.
-std::mutex g_attr_mu;
-struct AttrDone {
-  const void* kernel;
-  int device;
-};
-AttrDone g_attr_done[256];
-int g_attr_count = 0;
-
-template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const void* key = reinterpret_cast<const void*>(kernel);
-  std::lock_guard<std::mutex> lock(g_attr_mu);
-  for (int i = 0; i < g_attr_count; ++i)
-    if (g_attr_done[i].kernel == key && g_attr_done[i].device == dev) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && g_attr_count < 256) g_attr_done[g_attr_count++] = AttrDone{key, dev};
-  return e;
 }
 
 template <int D, bool C, int P>
@@ -510,6 +501,7 @@ const char* fa_strerror(int status) {
     case FA_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "device pipeline wait timed out";
+    case FA_ERR_INDEX: return "an index read on the device was out of range";
     default: return "unknown status";
   }
 }
@@ -739,7 +731,7 @@ int fa_last_device_status(void* stream, int* detail) {
     const int zero = 0;
     if (cudaMemcpy(status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return FA_ERR_CUDA;
     if (detail) *detail = v;
-    return FA_ERR_TIMEOUT;
+    return (v & ~0xFF) == fa::kSitePaged ? FA_ERR_INDEX : FA_ERR_TIMEOUT;
   }
   return FA_OK;
 }

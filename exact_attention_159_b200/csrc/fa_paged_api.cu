@@ -1,0 +1,290 @@
+// fa_paged_api.cu -- host side of the paged key/value cache: argument checks, plans, launches.
+// See include/fa.h for the contract of every entry point.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "fa_append.cuh"
+#include "fa_host.h"
+#include "fa_paged.cuh"
+#include "fa_paged_decode.cuh"
+
+using namespace fa_host;
+
+namespace {
+
+// Short caches (at most this many keys by the block table's width) are not cut along the keys: each CTA
+// takes whole items and nothing is joined.
+constexpr int kWholeKeys = 256;
+
+struct Sizes {
+  size_t cache, scales, table;
+};
+
+// Checks shared by both operators; *empty set when there is nothing to do.
+int check_paged(const fa_paged_cache* c, const fa_paged_batch* b, int T, int Hq, bool queries, bool* empty, Sizes* z) {
+  *empty = false;
+  if (!c || !b) return FA_ERR_INVALID_ARG;
+  if (c->type != FA_CACHE_BF16 && c->type != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->heads < 0 || b->B < 0 || b->max_pages < 0 || b->max_q < 0 || T < 0 || Hq < 0)
+    return FA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FA_ERR_UNSUPPORTED;
+  if (queries && (c->heads == 0 ? Hq != 0 : Hq % c->heads != 0)) return FA_ERR_INVALID_ARG;
+  if (T == 0 || b->B == 0 || c->heads == 0 || b->max_q == 0 || (queries && Hq == 0)) {
+    *empty = true;
+    return FA_OK;
+  }
+  if (!c->K || !c->V || !b->block_table || !b->cu_q || !b->seq_lens) return FA_ERR_INVALID_ARG;
+  if (c->type == FA_CACHE_E4M3 && (!c->K_scale || !c->V_scale)) return FA_ERR_INVALID_ARG;
+  if (c->num_pages == 0 || b->max_pages == 0) return FA_ERR_INVALID_ARG;
+  if (!aligned16(c->K) || !aligned16(c->V)) return FA_ERR_ALIGNMENT;
+  // int lengths and tensor-map extents stay in range
+  if (static_cast<long long>(c->num_pages) * c->heads > INT_MAX / 2) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(b->max_pages) * c->page_size > INT_MAX / 2) return FA_ERR_UNSUPPORTED;
+  z->cache = static_cast<size_t>(c->num_pages) * c->heads * c->page_size * c->d * (c->type == FA_CACHE_BF16 ? 2 : 1);
+  z->scales = static_cast<size_t>(c->num_pages) * c->heads * 4;
+  z->table = static_cast<size_t>(b->B) * b->max_pages * 4;
+  if (overlaps(c->K, z->cache, c->V, z->cache)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+// A written range against everything of the cache and the batch.
+bool meets(const void* p, size_t n, const fa_paged_cache* c, const fa_paged_batch* b, const Sizes& z) {
+  if (overlaps(p, n, c->K, z.cache) || overlaps(p, n, c->V, z.cache)) return true;
+  if (c->type == FA_CACHE_E4M3 && (overlaps(p, n, c->K_scale, z.scales) || overlaps(p, n, c->V_scale, z.scales)))
+    return true;
+  return overlaps(p, n, b->block_table, z.table) || overlaps(p, n, b->cu_q, static_cast<size_t>(b->B + 1) * 4) ||
+         overlaps(p, n, b->seq_lens, static_cast<size_t>(b->B) * 4);
+}
+
+size_t rows_bytes(int T, int64_t ld, int heads, int d) {
+  return (static_cast<size_t>(T - 1) * ld + static_cast<size_t>(heads) * d) * 2;
+}
+
+int shift_of(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
+fa::PagedBatch device_batch(const fa_paged_cache* c, const fa_paged_batch* b, int T, int* status) {
+  fa::PagedBatch p;
+  p.table = b->block_table;
+  p.cu_q = b->cu_q;
+  p.lens = b->seq_lens;
+  p.B = b->B;
+  p.T = T;
+  p.max_q = b->max_q;
+  p.max_pages = b->max_pages;
+  p.num_pages = c->num_pages;
+  p.page_shift = shift_of(c->page_size);
+  p.Hkv = c->heads;
+  p.status = status;
+  return p;
+}
+
+// 3-D map over the pages [num_pages * heads, page_size, d]: box of a row's 128 bytes (64 when a whole row
+// is 64 bytes) x `rows` slots, swizzled by the box's width.
+bool make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache* c, int rows) {
+  const bool fp8 = c->type == FA_CACHE_E4M3;
+  const MapKey key{base, c->num_pages * c->heads, c->page_size, c->d, rows, fp8 ? 3 : 2};
+  if (map_lookup(key, map)) return true;
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t size = fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->num_pages) * c->heads};
+  const cuuint64_t strides[2] = {c->d * size, static_cast<cuuint64_t>(c->page_size) * c->d * size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(fp8 ? c->d : 64), static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         fp8 && c->d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  map_store(key, *map);
+  return true;
+}
+
+template <int D, bool FP8>
+int launch_append(const fa::AppendParams& prm, long long grid, cudaStream_t st) {
+  const int items = max(1, (1 << prm.b.page_shift) * (D / 8) / fa::kAppendThreads);
+  const unsigned g = static_cast<unsigned>(grid);
+  switch (items) {
+    case 1: fa::append_kernel<D, FP8, 1><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
+    case 2: fa::append_kernel<D, FP8, 2><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
+    case 4: fa::append_kernel<D, FP8, 4><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
+    default: fa::append_kernel<D, FP8, 8><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+struct PagedWs {
+  size_t o, ml, total;
+};
+PagedWs paged_ws(int d, int n_cta) {
+  PagedWs w;
+  w.o = 0;
+  w.ml = round256(static_cast<size_t>(2) * n_cta * fa::kDecRows * d * 4);
+  w.total = w.ml + round256(static_cast<size_t>(2) * n_cta * fa::kDecRows * 8);
+  return w;
+}
+bool whole_items(const fa_paged_cache* c, const fa_paged_batch* b) {
+  return static_cast<long long>(b->max_pages) * c->page_size <= kWholeKeys;
+}
+
+template <int D, bool FP8>
+int launch_decode(const CUtensorMap& k, const CUtensorMap& v, const fa::DecodeParams& prm, int n_cta, cudaStream_t st) {
+  using L = fa::DecodeLayout<D, FP8>;
+  auto kern = fa::decode_kernel<D, FP8>;
+  if (set_smem(kern, L::kBytes) != cudaSuccess) return FA_ERR_CUDA;
+  kern<<<n_cta, fa::kDecThreads, L::kBytes, st>>>(k, v, prm);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (prm.whole || n_cta == 1) return FA_OK;
+  // the join may be scheduled while the shares run; it waits for them before it reads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_cta - 1);
+  cfg.blockDim = dim3(fa::kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa::decode_join_kernel<D>, prm, n_cta) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, const void* K, int64_t ldk,
+                    const void* V, int64_t ldv, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo, int Hq,
+                    const float* cosine, const float* sine, int rot_dim, int interleaved, int n_pos, void* stream) {
+  bool empty = false;
+  Sizes z;
+  int rc = check_paged(cache, batch, T, Hq, Q != nullptr, &empty, &z);
+  if (rc != FA_OK) return rc;
+  if (rot_dim < 0 || n_pos < 0 || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+  if (rot_dim > cache->d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if ((Q == nullptr) != (Q_out == nullptr) || (Q ? rot_dim == 0 : Hq != 0)) return FA_ERR_INVALID_ARG;
+  if (empty) return FA_OK;
+  if (!K || !V || (rot_dim > 0 && (!cosine || !sine))) return FA_ERR_INVALID_ARG;
+  const int Hkv = cache->heads, d = cache->d;
+  const int64_t kv_row = static_cast<int64_t>(Hkv) * d, q_row = static_cast<int64_t>(Hq) * d;
+  if (ldk < kv_row || ldv < kv_row || (Q && (ldq < q_row || ldqo < q_row))) return FA_ERR_INVALID_ARG;
+  if (ldk % 8 || ldv % 8 || (Q && (ldq % 8 || ldqo % 8))) return FA_ERR_ALIGNMENT;
+  for (const void* p : {K, V, Q, static_cast<const void*>(Q_out), static_cast<const void*>(rot_dim ? cosine : nullptr),
+                        static_cast<const void*>(rot_dim ? sine : nullptr)})
+    if (!aligned16(p)) return FA_ERR_ALIGNMENT;
+  for (const int64_t ld : {ldk, ldv, Q ? ldq : 0, Q ? ldqo : 0})
+    if (ld > (1LL << 40) / T) return FA_ERR_UNSUPPORTED;
+  const size_t kb = rows_bytes(T, ldk, Hkv, d), vb = rows_bytes(T, ldv, Hkv, d);
+  const size_t tb = static_cast<size_t>(n_pos) * (rot_dim / 2) * 4;
+  if (meets(K, kb, cache, batch, z) || meets(V, vb, cache, batch, z)) return FA_ERR_INVALID_ARG;
+  if (Q) {
+    const size_t qb = rows_bytes(T, ldq, Hq, d), ob = rows_bytes(T, ldqo, Hq, d);
+    if (meets(Q, qb, cache, batch, z) || meets(Q_out, ob, cache, batch, z)) return FA_ERR_INVALID_ARG;
+    // in place the rows of a fused projection lie between K's and V's, and only Q's own elements are written
+    if (!(Q_out == Q && ldqo == ldq) &&
+        (overlaps(Q_out, ob, Q, qb) || overlaps(Q_out, ob, K, kb) || overlaps(Q_out, ob, V, vb)))
+      return FA_ERR_INVALID_ARG;
+    if (overlaps(Q_out, ob, cosine, tb) || overlaps(Q_out, ob, sine, tb)) return FA_ERR_INVALID_ARG;
+  }
+  if (rot_dim && (meets(cosine, tb, cache, batch, z) || meets(sine, tb, cache, batch, z))) return FA_ERR_INVALID_ARG;
+  int* status = device_status(&rc);
+  if (!status) return rc;
+  fa::AppendParams prm;
+  prm.b = device_batch(cache, batch, T, status);
+  prm.K = static_cast<const __nv_bfloat16*>(K);
+  prm.V = static_cast<const __nv_bfloat16*>(V);
+  prm.Q = static_cast<const __nv_bfloat16*>(Q);
+  prm.Qo = static_cast<__nv_bfloat16*>(Q_out);
+  prm.ldk = ldk;
+  prm.ldv = ldv;
+  prm.ldq = ldq;
+  prm.ldqo = ldqo;
+  prm.cosp = cosine;
+  prm.sinp = sine;
+  prm.rot = rot_dim;
+  prm.interleaved = interleaved;
+  prm.n_pos = n_pos;
+  prm.Kc = cache->K;
+  prm.Vc = cache->V;
+  prm.Ks = cache->K_scale;
+  prm.Vs = cache->V_scale;
+  prm.G = Q ? Hq / Hkv : 0;
+  // max_q consecutive slots starting anywhere in a page, no more than the table is wide
+  const int most = batch->max_q < T ? batch->max_q : T;
+  prm.max_touched = (most + cache->page_size - 2) / cache->page_size + 1;
+  if (prm.max_touched > batch->max_pages) prm.max_touched = batch->max_pages;
+  const long long grid = static_cast<long long>(batch->B) * prm.max_touched * Hkv;
+  if (grid > INT_MAX) return FA_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool fp8 = cache->type == FA_CACHE_E4M3;
+  if (d == 128) return fp8 ? launch_append<128, true>(prm, grid, st) : launch_append<128, false>(prm, grid, st);
+  return fp8 ? launch_append<64, true>(prm, grid, st) : launch_append<64, false>(prm, grid, st);
+}
+
+size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, int Hq) {
+  bool empty = false;
+  Sizes z;
+  if (check_paged(cache, batch, T, Hq, true, &empty, &z) != FA_OK || empty) return 0;
+  return paged_ws(cache->d, fa::kDecCtas).total;
+}
+
+int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const fa_paged_batch* batch, int T, void* O,
+                 float* LSE, void* workspace, size_t workspace_bytes, int Hq, float scale, int causal, void* stream) {
+  bool empty = false;
+  Sizes z;
+  int rc = check_paged(cache, batch, T, Hq, true, &empty, &z);
+  if (rc != FA_OK) return rc;
+  if ((causal != 0 && causal != 1) || !(scale > 0.0f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (empty) return FA_OK;
+  if (!Q || !O || !LSE || !workspace) return FA_ERR_INVALID_ARG;
+  if (ldq < static_cast<int64_t>(Hq) * cache->d) return FA_ERR_INVALID_ARG;
+  if (ldq % 8 || !aligned16(Q) || !aligned16(O) || !aligned16(LSE) || !aligned16(workspace)) return FA_ERR_ALIGNMENT;
+  if (ldq > (1LL << 40) / T || static_cast<long long>(T) * Hq > INT_MAX) return FA_ERR_UNSUPPORTED;
+  const int n_cta = fa::kDecCtas;
+  const PagedWs ws = paged_ws(cache->d, n_cta);
+  if (workspace_bytes < ws.total) return FA_ERR_INVALID_ARG;
+  const size_t qb = rows_bytes(T, ldq, Hq, cache->d), ob = static_cast<size_t>(T) * Hq * cache->d * 2;
+  const size_t lb = static_cast<size_t>(T) * Hq * 4;
+  const void* outs[3] = {O, LSE, workspace};
+  const size_t osz[3] = {ob, lb, ws.total};
+  for (int i = 0; i < 3; ++i) {
+    if (meets(outs[i], osz[i], cache, batch, z) || overlaps(outs[i], osz[i], Q, qb)) return FA_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(outs[i], osz[i], outs[j], osz[j])) return FA_ERR_INVALID_ARG;
+  }
+  int* status = device_status(&rc);
+  if (!status) return rc;
+  const int box = cache->page_size < fa::kDecTile ? cache->page_size : fa::kDecTile;
+  CUtensorMap mk, mv;
+  if (!make_page_map(&mk, cache->K, cache, box) || !make_page_map(&mv, cache->V, cache, box)) return FA_ERR_CUDA;
+  fa::DecodeParams prm;
+  prm.b = device_batch(cache, batch, T, status);
+  prm.Q = static_cast<const __nv_bfloat16*>(Q);
+  prm.ldq = ldq;
+  prm.O = static_cast<__nv_bfloat16*>(O);
+  prm.LSE = LSE;
+  prm.Ks = cache->K_scale;
+  prm.Vs = cache->V_scale;
+  prm.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.o);
+  prm.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ml);
+  prm.G = Hq / cache->heads;
+  prm.Hq = Hq;
+  prm.max_rows = INT_MAX;
+  prm.causal = causal;
+  prm.whole = whole_items(cache, batch) ? 1 : 0;
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool fp8 = cache->type == FA_CACHE_E4M3;
+  if (cache->d == 128)
+    return fp8 ? launch_decode<128, true>(mk, mv, prm, n_cta, st) : launch_decode<128, false>(mk, mv, prm, n_cta, st);
+  return fp8 ? launch_decode<64, true>(mk, mv, prm, n_cta, st) : launch_decode<64, false>(mk, mv, prm, n_cta, st);
+}
+
+}  // extern "C"

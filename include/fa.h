@@ -49,7 +49,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2, /* head dim other than 64/128, sizes beyond the index range */
   FA_ERR_ALIGNMENT = 3,   /* a pointer not 16-byte aligned */
   FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed (launch, attributes, TMA encode) */
-  FA_ERR_TIMEOUT = 5      /* a kernel's bounded pipeline wait expired (see fa_last_device_status) */
+  FA_ERR_TIMEOUT = 5,     /* a kernel's bounded pipeline wait expired (see fa_last_device_status) */
+  FA_ERR_INDEX = 6        /* an index that a kernel read from device memory was out of range (paged cache) */
 } fa_status;
 
 /*
@@ -207,6 +208,119 @@ int fa_accumulate_f32(float* acc, const float* x, int64_t n, void* stream);
 /* y (bf16, n) = x (fp32, n) rounded to nearest even; n a multiple of 8, both 16-byte aligned. */
 int fa_convert_f32_bf16(const float* x, void* y, int64_t n, void* stream);
 
+/*
+ * The paged key/value cache: keys and values of many sequences in pages taken
+ * from one pool, so that sequences grow by a token or a prompt chunk at a time
+ * without moving.  fa_cache_append writes new tokens into it, fa_fwd_paged
+ * attends to it.
+ *
+ * fa_paged_cache: K, V [num_pages, heads, page_size, d], contiguous, 16-byte
+ * aligned, of `type`: FA_CACHE_BF16, or FA_CACHE_E4M3 (8-bit floating point,
+ * finite range +-448) with K_scale, V_scale fp32 [num_pages, heads]: a held
+ * value stands for code * scale, one scale for the block of tokens and head
+ * that a page holds.  heads: key/value heads.  page_size 16, 32, 64 or 128;
+ * d 64 or 128.  K_scale and V_scale are not read for a bf16 cache.
+ *
+ * fa_paged_batch: B sequences.  cu_q int32 [B + 1]: sequence b's new tokens are
+ * rows cu_q[b] .. cu_q[b+1] - 1 of the token-major tensors of T rows (T >=
+ * cu_q[B]; rows behind cu_q[B] are neither read nor written).  seq_lens int32
+ * [B]: tokens of the sequence in all, the new ones last.  block_table int32
+ * [B, max_pages]: token p of sequence b is in slot p % page_size of page
+ * block_table[b][p / page_size]; entries behind the last token's are not read.
+ * max_q: no sequence has more new tokens.  All three arrays are DEVICE memory
+ * and are read when the kernels run, so a captured call replays with new
+ * contents.
+ *
+ * The kernels check what they read there: a cu_q that decreases, leaves [0, T]
+ * or exceeds max_q (detail 0xE01: that sequence is left out), a length below
+ * zero, beyond the table or, in fa_cache_append, below the new tokens (0xE02),
+ * a page number outside [0, num_pages) (0xE03: its tokens are not written; in
+ * fa_fwd_paged that sequence's results are unspecified), a position beyond the
+ * rotation's tables (0xE04: the token is left out).  fa_last_device_status
+ * reports them as FA_ERR_INDEX; memory outside the given tensors is never
+ * touched.
+ */
+#define FA_CACHE_BF16 0
+#define FA_CACHE_E4M3 1
+
+typedef struct {
+  void* K;
+  void* V;
+  float* K_scale;
+  float* V_scale;
+  int type;
+  int num_pages;
+  int heads;
+  int page_size;
+  int d;
+} fa_paged_cache;
+
+typedef struct {
+  const int* block_table;
+  const int* cu_q;
+  const int* seq_lens;
+  int B;
+  int max_pages;
+  int max_q;
+} fa_paged_batch;
+
+/*
+ * Appends the new tokens' keys and values to the cache, the keys rotated by
+ * their positions on the way; rotates the queries of the same tokens too when
+ * Q is given.  A sequence's new tokens take positions seq_lens[b] - (new
+ * tokens) .. seq_lens[b] - 1.
+ *
+ * K, V: bf16 [T, heads, d], row t at K + t * ldk elements (ldk, ldv >= heads *
+ * d, multiples of 8), so slices of a fused projection serve as they are.  Q:
+ * bf16 [T, Hq, d], rows ldq apart, or NULL; Q_out: bf16 [T, Hq, d], rows ldqo
+ * apart (Q_out == Q with ldqo == ldq rotates in place).  Hq a multiple of
+ * heads (0 without Q).
+ * cosine, sine: fp32 [n_pos, rot_dim / 2], 16-byte aligned, the angles' cosines and sines
+ * of each position; rot_dim <= d, a multiple of 16 (0: no rotation, and no Q).
+ * The first rot_dim columns turn in pairs, x_i' = x_i cos - x_j sin, x_j' =
+ * x_j cos + x_i sin, with (i, j) = (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * interleaved = 1; pair i uses column i of the tables.  fp32 arithmetic.
+ *
+ * bf16 cache: one rounding.  e4m3 cache: for every page and head that gets
+ * tokens, scale' = max(scale, s) when the page already holds earlier tokens of
+ * the sequence, s otherwise, where s is the smallest power of two >= 2^-100
+ * with every new finite |value| <= 448 s; new codes are e4m3(value / scale')
+ * (an infinity becomes +-448, a NaN stays one), and when the scale grew the
+ * earlier codes become e4m3(code * scale / scale'), which changes only what
+ * falls among e4m3's subnormals.  Slots behind the new tokens keep their bytes.
+ *
+ * A page that one call writes must belong to one sequence (and once to it):
+ * two sequences that share pages may share full ones only.  Q_out may not
+ * overlap the cache or, unless in place, Q; nor the cache any input.  One
+ * launch.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
+ */
+int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, const void* K, int64_t ldk,
+                    const void* V, int64_t ldv, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo, int Hq,
+                    const float* cosine, const float* sine, int rot_dim, int interleaved, int n_pos, void* stream);
+
+/*
+ * Attention of the new tokens' queries over their sequences in the cache:
+ * single tokens, a few drafted tokens, prompt chunks, or all of them in one
+ * batch.  Q: bf16 [T, Hq, d], rows ldq elements apart (>= Hq * d, a multiple
+ * of 8); O: bf16 [T, Hq, d] contiguous; LSE: fp32 [T, Hq], natural log.  Query
+ * head h reads key/value head h / (Hq / heads).  With causal = 1, new token i
+ * of a sequence sees its keys up to position seq_lens[b] - (new tokens) + i;
+ * with 0 it sees them all.  A row that sees no key (a sequence of length 0, or
+ * shorter than its new tokens) gets O = 0, LSE = -inf.  Slots behind a
+ * sequence's end may hold anything, NaN included.  Keys and values of live
+ * tokens, queries and scales must be finite: one that is not may reach every
+ * row of its sequence.  For an e4m3 cache any finite scales >= 0 serve (value
+ * scales below 2^-100 count as 2^-100).
+ *
+ * workspace: device memory of at least fa_fwd_paged_workspace_size() bytes,
+ * 16-byte aligned; contents on entry do not matter, and calls that may overlap
+ * in time must not share one (two captured graphs included).  The size depends
+ * on (heads, d, page_size, Hq, T, B, max_pages, max_q) only.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
+ */
+size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, int Hq);
+int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const fa_paged_batch* batch, int T, void* O,
+                 float* LSE, void* workspace, size_t workspace_bytes, int Hq, float scale, int causal, void* stream);
+
 /* Static human-readable text for a status code. */
 const char* fa_strerror(int status);
 
@@ -214,8 +328,10 @@ const char* fa_strerror(int status);
  * Synchronises `stream`, then reports device-side failures since the last
  * call on the current device: FA_ERR_TIMEOUT if a kernel's bounded wait
  * expired (the detail code, kernel and wait site, is returned through
- * *detail when detail is not NULL), FA_ERR_CUDA if the synchronisation
- * itself failed, FA_OK otherwise.  Clears the recorded failure.
+ * *detail when detail is not NULL), FA_ERR_INDEX if a kernel of the paged
+ * cache met an index out of range (detail: see the paged cache), FA_ERR_CUDA
+ * if the synchronisation itself failed, FA_OK otherwise.  The first failure
+ * is the one kept.  Clears the recorded failure.
  */
 int fa_last_device_status(void* stream, int* detail);
 

@@ -1,0 +1,132 @@
+"""The paged cache's refusals on the host (CPU only): nothing here reaches a kernel."""
+import ctypes
+
+import pytest
+import torch
+
+from exact_attention_159_b200 import _lib, api, build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.lib()
+
+
+A = [0x1000000 * (i + 1) for i in range(16)]  # fake, 16-byte aligned: never dereferenced by the checks
+
+
+def cache(e4m3=True, **kw):
+    c = dict(K=A[0], V=A[1], K_scale=A[2], V_scale=A[3], type=int(e4m3), num_pages=10, heads=2, page_size=16, d=64)
+    c.update(kw)
+    return _lib.CacheStruct(*(c[n] for n, _ in _lib.CacheStruct._fields_))
+
+
+def batch(**kw):
+    b = dict(block_table=A[4], cu_q=A[5], seq_lens=A[6], B=3, max_pages=4, max_q=5)
+    b.update(kw)
+    return _lib.BatchStruct(*(b[n] for n, _ in _lib.BatchStruct._fields_))
+
+
+def append(lib, c=None, b=None, T=6, K=A[7], ldk=128, V=A[8], ldv=128, Q=None, ldq=0, Qo=None, ldqo=0, Hq=0, cos=None,
+           sin=None, rot=0, inter=0, n_pos=0):
+    c, b = c or cache(), b or batch()
+    return lib.fa_cache_append(ctypes.byref(c), ctypes.byref(b), T, K, ldk, V, ldv, Q, ldq, Qo, ldqo, Hq, cos, sin, rot,
+                               inter, n_pos, None)
+
+
+Q_ARGS = dict(Q=A[9], ldq=256, Qo=A[10], ldqo=256, Hq=4, cos=A[11], sin=A[12], rot=64, n_pos=100)
+INVALID, UNSUPPORTED, ALIGN, OK = (_lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED, _lib.FA_ERR_ALIGNMENT, _lib.FA_OK)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(c=cache(type=2)), INVALID), (dict(c=cache(d=96)), UNSUPPORTED), (dict(c=cache(d=256)), UNSUPPORTED),
+    (dict(c=cache(page_size=8)), UNSUPPORTED), (dict(c=cache(page_size=48)), UNSUPPORTED),
+    (dict(c=cache(num_pages=-1)), INVALID), (dict(c=cache(num_pages=0)), INVALID), (dict(c=cache(heads=-2)), INVALID),
+    (dict(c=cache(num_pages=1 << 30)), UNSUPPORTED), (dict(c=cache(K=None)), INVALID),
+    (dict(c=cache(K_scale=None)), INVALID), (dict(c=cache(V=A[1] + 8)), ALIGN), (dict(c=cache(V=A[0] + 64)), INVALID),
+    (dict(b=batch(B=-1)), INVALID), (dict(b=batch(max_q=-1)), INVALID), (dict(b=batch(max_pages=0)), INVALID),
+    (dict(b=batch(max_pages=1 << 28)), UNSUPPORTED), (dict(b=batch(cu_q=None)), INVALID), (dict(T=-1), INVALID),
+    (dict(b=batch(block_table=None)), INVALID), (dict(b=batch(seq_lens=None)), INVALID),
+    (dict(K=None), INVALID), (dict(ldk=120), INVALID), (dict(ldv=64), INVALID), (dict(ldk=132), ALIGN),
+    (dict(K=A[7] + 8), ALIGN), (dict(V=A[0]), INVALID), (dict(K=A[4]), INVALID), (dict(Hq=4), INVALID),
+    (dict(rot=8), UNSUPPORTED), (dict(rot=80), UNSUPPORTED), (dict(rot=-16), INVALID), (dict(inter=2), INVALID),
+    (dict(rot=64, cos=None, sin=A[12]), INVALID), (dict(rot=64, cos=A[11] + 4, sin=A[12], n_pos=9), ALIGN),
+    (dict(n_pos=-1), INVALID), (dict(ldk=1 << 50), UNSUPPORTED),
+    (dict(Q_ARGS, Qo=None), INVALID), (dict(Q_ARGS, Hq=3), INVALID), (dict(Q_ARGS, rot=0), INVALID),
+    (dict(Q_ARGS, ldq=128), INVALID), (dict(Q_ARGS, ldqo=260), ALIGN), (dict(Q_ARGS, Qo=A[9] + 16), INVALID),
+    (dict(Q_ARGS, Qo=A[9], ldqo=512), INVALID), (dict(Q_ARGS, Qo=A[7]), INVALID), (dict(Q_ARGS, Qo=A[0]), INVALID),
+    (dict(Q_ARGS, Qo=A[2]), INVALID), (dict(Q_ARGS, Qo=A[11]), INVALID), (dict(Q_ARGS, cos=A[1]), INVALID),
+])
+def test_append_refusals(lib, bad, code):
+    assert append(lib, **bad) == code
+
+
+def test_empty_appends(lib):
+    assert append(lib, T=0) == OK and append(lib, b=batch(B=0)) == OK
+    assert append(lib, c=cache(heads=0)) == OK and append(lib, b=batch(max_q=0)) == OK
+    assert append(lib, c=cache(d=80), T=0) == UNSUPPORTED  # what is wrong is wrong with nothing to do too
+    assert lib.fa_cache_append(None, None, 1, None, 0, None, 0, None, 0, None, 0, 0, None, None, 0, 0, 0, None) == INVALID
+
+
+def fwd(lib, c=None, b=None, T=6, Q=A[7], ldq=256, O=A[8], L=A[9], W=A[10], wsb=1 << 30, Hq=4, scale=0.125, causal=1):
+    c, b = c or cache(), b or batch()
+    return lib.fa_fwd_paged(Q, ldq, ctypes.byref(c), ctypes.byref(b), T, O, L, W, wsb, Hq, scale, causal, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(Hq=5), INVALID), (dict(Hq=-4), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(causal=2), INVALID), (dict(Q=None), INVALID), (dict(L=None), INVALID),
+    (dict(W=None), INVALID), (dict(ldq=128), INVALID), (dict(ldq=260), ALIGN), (dict(Q=A[7] + 8), ALIGN),
+    (dict(O=A[8] + 4), ALIGN), (dict(L=A[9] + 4), ALIGN), (dict(W=A[10] + 8), ALIGN), (dict(O=A[0]), INVALID),
+    (dict(O=A[7]), INVALID), (dict(L=A[8]), INVALID), (dict(W=A[3]), INVALID), (dict(W=A[4]), INVALID),
+    (dict(c=cache(type=-1)), INVALID), (dict(c=cache(page_size=256)), UNSUPPORTED), (dict(wsb=16), INVALID),
+    (dict(c=cache(V_scale=None)), INVALID), (dict(T=1 << 30, Hq=4), UNSUPPORTED),
+])
+def test_attention_refusals(lib, bad, code):
+    assert fwd(lib, **bad) == code
+
+
+def test_empty_attention(lib):
+    assert fwd(lib, T=0) == OK and fwd(lib, b=batch(B=0)) == OK and fwd(lib, b=batch(max_q=0)) == OK
+    assert fwd(lib, c=cache(heads=0), Hq=0) == OK and fwd(lib, c=cache(heads=0), Hq=4) == INVALID
+    c, b = cache(d=96), batch()
+    assert lib.fa_fwd_paged_workspace_size(ctypes.byref(c), ctypes.byref(b), 6, 4) == 0
+
+
+def test_strerror_of_the_index_status(lib):
+    assert lib.fa_strerror(_lib.FA_ERR_INDEX) != b"unknown status"
+
+
+# --------------------------------------------------------------------------------- the torch binding
+def test_cpu_tensors_and_wrong_kinds_are_refused():
+    pages = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.PagedCache(pages, pages.clone())
+    with pytest.raises(ValueError, match="float8_e4m3fn"):
+        api.PagedCache(pages.float(), pages.float())
+    with pytest.raises(ValueError, match="page_size"):
+        api.PagedCache(pages[:, :, :8], pages[:, :, :8])
+    with pytest.raises(ValueError):
+        api.PagedCache(pages[0], pages[0])
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match="CUDA"):
+        api.PagedBatch(i(2, 3), i(3), i(2), 1)
+    with pytest.raises(ValueError):
+        api.PagedBatch(i(2), i(3), i(2), 1)
+
+
+# ------------------------------------------------------------------ the device's plans, run on the host
+def test_plans_on_the_host(tmp_path):
+    """Compiles the kernels' index arithmetic (csrc/fa_paged*.cuh) for the host and runs it over many batches:
+    bad lengths, rows and pages are refused, every tile of every item is in exactly one share, and every item
+    that a cut divides is joined once, from exactly the slots its parts were left in."""
+    import os
+    import subprocess
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "plan")
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "-O1", "-I", build.CSRC, "-o", exe,
+                    os.path.join(here, "paged_plan_host.cu")], check=True, capture_output=True, text=True)
+    done = subprocess.run([exe], capture_output=True, text=True)
+    assert done.returncode == 0, done.stdout + done.stderr
+    assert "ok" in done.stdout
