@@ -107,7 +107,8 @@ __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float ratio
     uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = half2_of_e4m3(w[j]), hi = half2_of_e4m3(w[j] >> 16);
+      uint32_t lo, hi;
+      halves_of_e4m3(w[j], lo, hi);
       const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
       const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
       w[j] = e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(b.x * ratio, b.y * ratio) << 16);

@@ -79,10 +79,12 @@ FA_HD int load_page(const PagedBatch& p, int b, int i) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-// The two e4m3 values of the low 16 bits as halves (exact: e4m3's values and subnormals are normal halves).
-__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xFFFFu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// The four e4m3 values of a word as halves (exact: e4m3's values and subnormals are normal halves), the low
+// two in `lo`.
+__device__ __forceinline__ void halves_of_e4m3(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 
 // The smallest scale a page gets, and the exponent of the smallest power of two 2^e >= 2^kScaleMinExp with

@@ -135,10 +135,10 @@ bool whole_items(const fa_paged_cache* c, const fa_paged_batch* b) {
   return static_cast<long long>(b->max_pages) * c->page_size <= kWholeKeys;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 int launch_decode(const CUtensorMap& k, const CUtensorMap& v, const fa::DecodeParams& prm, int n_cta, cudaStream_t st) {
   using L = fa::DecodeLayout<D, FP8>;
-  auto kern = fa::decode_kernel<D, FP8>;
+  auto kern = fa::decode_kernel<D, FP8, NT>;
   if (set_smem(kern, L::kBytes) != cudaSuccess) return FA_ERR_CUDA;
   kern<<<n_cta, fa::kDecThreads, L::kBytes, st>>>(k, v, prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
@@ -154,6 +154,14 @@ int launch_decode(const CUtensorMap& k, const CUtensorMap& v, const fa::DecodePa
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fa::decode_join_kernel<D>, prm, n_cta) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int NT>
+int launch_decode_type(int d, bool fp8, const CUtensorMap& k, const CUtensorMap& v, const fa::DecodeParams& prm,
+                       int n_cta, cudaStream_t st) {
+  if (d == 128)
+    return fp8 ? launch_decode<128, true, NT>(k, v, prm, n_cta, st) : launch_decode<128, false, NT>(k, v, prm, n_cta, st);
+  return fp8 ? launch_decode<64, true, NT>(k, v, prm, n_cta, st) : launch_decode<64, false, NT>(k, v, prm, n_cta, st);
 }
 
 }  // namespace
@@ -261,7 +269,9 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   }
   int* status = device_status(&rc);
   if (!status) return rc;
-  const int box = cache->page_size < fa::kDecTile ? cache->page_size : fa::kDecTile;
+  const bool fp8 = cache->type == FA_CACHE_E4M3;
+  const int tile = fp8 ? fa::DecodeLayout<128, true>::kTile : fa::DecodeLayout<128, false>::kTile;
+  const int box = cache->page_size < tile ? cache->page_size : tile;
   CUtensorMap mk, mv;
   if (!make_page_map(&mk, cache->K, cache, box) || !make_page_map(&mv, cache->V, cache, box)) return FA_ERR_CUDA;
   fa::DecodeParams prm;
@@ -276,15 +286,15 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   prm.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ml);
   prm.G = Hq / cache->heads;
   prm.Hq = Hq;
+  prm.tile = tile;
+  prm.rows = static_cast<long long>(batch->max_q) * prm.G <= 8 ? 8 : 16;
   prm.max_rows = INT_MAX;
   prm.causal = causal;
   prm.whole = whole_items(cache, batch) ? 1 : 0;
   prm.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool fp8 = cache->type == FA_CACHE_E4M3;
-  if (cache->d == 128)
-    return fp8 ? launch_decode<128, true>(mk, mv, prm, n_cta, st) : launch_decode<128, false>(mk, mv, prm, n_cta, st);
-  return fp8 ? launch_decode<64, true>(mk, mv, prm, n_cta, st) : launch_decode<64, false>(mk, mv, prm, n_cta, st);
+  if (prm.rows == 8) return launch_decode_type<1>(cache->d, fp8, mk, mv, prm, n_cta, st);
+  return launch_decode_type<2>(cache->d, fp8, mk, mv, prm, n_cta, st);
 }
 
 }  // extern "C"

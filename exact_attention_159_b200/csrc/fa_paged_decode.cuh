@@ -2,29 +2,32 @@
 // cache: one pass over the keys and values with a running maximum and sum, the long axis split evenly
 // over the GPU and joined by a second small kernel.
 //
-// With few rows the work is reading the cache once, so everything here serves that: TMA brings 64-key
-// tiles of a page list into a ring of shared-memory stages (96 KB of loads in flight per CTA, two CTAs an
-// SM), and the arithmetic runs on mma.sync m16n8k16, whose 16 rows fit the query heads that share a
-// key/value head, where a tcgen05 tile would be 128 rows of padding.
+// With few rows the work is reading the cache once, so everything here serves that: TMA brings tiles of
+// 64 keys (bf16) or 128 keys (e4m3) of a page list into a ring of shared-memory stages (96 KB of loads in
+// flight per CTA, two CTAs an SM), and the arithmetic runs on mma.sync m16n8k16 with keys (then value
+// columns) as its 16 rows and the query rows as its 8 columns: the query heads that share a key/value head
+// fit one or two such column tiles, where a tcgen05 tile would be 128 rows of padding.
 //
-// Rows: the R = rows * G (token, query head) pairs that read one key/value head, in blocks of 16.  One
-// (sequence, row block, key/value head) is an item of ceil(len / 64) tiles; the items' tiles laid end to
+// Rows: the R = rows * G (token, query head) pairs that read one key/value head, in blocks of 8 * NT.  One
+// (sequence, row block, key/value head) is an item of ceil(len / tile) tiles; the items' tiles laid end to
 // end are cut into equal runs, one per CTA, so a batch of ragged lengths loads every SM alike.  An item
 // that a cut divides leaves its unnormalised sums in the workspace, at most two a CTA, for the join.
 //
-// Each of the four consumer warps takes 16 keys of every tile and keeps its own maximum, sum and output
-// accumulators; they meet once, at the item's end.
-//   S = Q K^T:  A = Q (16 rows, registers for the whole item), B = 16 keys
-//   O += P V:   A = P straight from S's accumulators, B = V
+// Each of the four consumer warps takes a quarter of every tile's keys and keeps its own maximum, sum and
+// output accumulators; they meet once, at the item's end.
+//   S^T = K Q^T:   A = 16 keys, B = Q (registers for the whole item)
+//   O^T += V^T P^T: A = 16 columns of 16 values, B = P^T, S^T's accumulators transposed 8 x 8 at a time
+// The maximum is a reference that moves only when a score passes it by 2^8 (as in the other forwards): the
+// lanes of a row then agree on the new one; otherwise no lane has to ask another.
 // e4m3 pages: codes become halves exactly (one conversion for two codes) and the scales stay outside the
-// products: K's multiplies the scores, V's joins the exponent, w = 2^(s + log2 vs - m), so w <= 1 whatever
+// products: K's multiplies the scores, V's joins the exponent, w = 2^(s + log2 vs - m), so w <= 2^8 whatever
 // the scales, O = sum w * code, and the softmax's sum is sum w / vs.  Q is brought to [-1, 1] by a power of
 // two per row before it becomes halves.  P is rounded to half (11 bits; bf16 for a bf16 cache, as the
 // other forwards round it); m, the sums and O are fp32.
-// To feed B from bytes without a transposing load, columns are permuted: a lane's 16-byte chunk of a key
-// row holds its k indices of four MMAs, and a lane's 16-byte chunk of a value row holds its column n of
-// 16 output tiles.  Keys 0..7 of a tile's octet go to n = 0,2,4,6,1,3,5,7, which with TMA's 128-byte
-// swizzle puts the eight lanes of a load phase on eight different chunks.
+// To feed A from bytes without a transposing load, columns are permuted: a lane's 16-byte chunk of a key
+// row holds its k indices of four MMAs, and a lane's 16-byte chunk of a value row holds its rows of eight
+// output tiles.  Keys 0..7 of an octet go to rows 0,2,4,6,1,3,5,7, which with TMA's 128-byte swizzle puts
+// the eight lanes of a load phase on eight different chunks.
 #pragma once
 
 #include "exp2_poly.cuh"
@@ -33,12 +36,12 @@
 namespace fa {
 
 constexpr int kSiteDecode = 0xD00;
-constexpr int kDecTile = 64;       // keys of a tile
-constexpr int kDecRows = 16;       // query rows of an item
+constexpr int kDecRows = 16;       // most query rows of an item
 constexpr int kDecCtas = 2 * 148;  // two on each SM
 constexpr int kDecThreads = 160;   // four consumer warps, one producer warp
 constexpr int kDecStageBytes = 98304;
 constexpr int kDecMinTiles = 2;    // a CTA's share is at least this many tiles
+constexpr float kDecTau = 8.0f;    // log2 units
 constexpr float kScaleFloor = 7.8886090522101181e-31f;  // 2^-100: smaller value scales count as this
 
 struct DecodeParams {
@@ -48,9 +51,10 @@ struct DecodeParams {
   __nv_bfloat16* O;   // [T, Hq, D]
   float* LSE;         // [T, Hq]
   const float *Ks, *Vs;
-  float* part_o;      // [2 * n_cta][16][D] unnormalised sums
-  float2* part_ml;    // [2 * n_cta][16] (m in log2 units, l)
+  float* part_o;      // [2 * n_cta][rows][D] unnormalised sums
+  float2* part_ml;    // [2 * n_cta][rows] (m in log2 units, l)
   int G, Hq;
+  int tile, rows;     // keys of a tile (DecodeLayout::kTile), query rows of an item (8 * NT)
   int max_rows;       // sequences of more rows * G are another kernel's
   int causal, whole;  // whole: shares are whole items (short caches), nothing is joined
   float scale_log2;
@@ -58,17 +62,20 @@ struct DecodeParams {
 
 template <int D, bool FP8>
 struct DecodeLayout {
+  static constexpr int kTile = FP8 ? 128 : 64;       // keys: a quarter is one warp's, 32 or 16
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
-  static constexpr int kHalf = kDecTile * 128;  // bytes of a 128-byte-wide column block of a tile
-  static constexpr int kTileBytes = kDecTile * kRowBytes;
-  static constexpr int kStages = kDecStageBytes / (2 * kTileBytes) < 6 ? kDecStageBytes / (2 * kTileBytes) : 6;
+  static constexpr int kHalf = kTile * 128;          // bytes of a 128-byte-wide column block of a tile
+  static constexpr int kTileBytes = kTile * kRowBytes;
+  static constexpr int kStages = kDecStageBytes / (2 * kTileBytes);
+  static constexpr int kBoxes = kTile / 16;          // pages of a tile, at most
   static constexpr int kV = kStages * kTileBytes;
-  static constexpr int kMerge = 2 * kV;                      // two warps' accumulators
-  static constexpr int kMergeWarp = 16 * D * 4 + 512;        // float4 per lane and column tile, then (m, l) x 2
-  static constexpr int kMeta = kMerge + 2 * kMergeWarp;      // [stage][4 boxes] (K scale, V scale)
-  static constexpr int kBar = kMeta + kStages * 4 * 8;
+  static constexpr int kMerge = 2 * kV;              // two warps' accumulators, eight query rows at a time
+  static constexpr int kMergeWarp = (D / 16) * 512 + 512;  // a float4 per lane and column tile, then (m, l) x 2
+  static constexpr int kMeta = kMerge + 2 * kMergeWarp;    // [stage][box] (K scale, log2 V scale, 1 / V scale, -)
+  static constexpr int kBar = kMeta + kStages * kBoxes * 16;
   static constexpr int kMisc = kBar + 2 * kStages * 8;
   static constexpr int kBytes = kMisc + 96;
+  static_assert(kBytes <= (233472 - 2 * 1024) / 2, "two CTAs must fit an SM");
 };
 
 // ------------------------------------------------------------------------------------- the plan
@@ -81,8 +88,8 @@ FA_HD DecodeSeq decode_seq(const DecodeParams& p, int b) {
   d.s = load_seq(p.b, b);
   const long long rows = static_cast<long long>(d.s.rows) * p.G;
   const bool mine = rows > 0 && rows <= p.max_rows;
-  d.tiles = max(1, (d.s.len + kDecTile - 1) / kDecTile);  // a sequence of no keys still gets its rows written
-  d.items = mine ? static_cast<int>((rows + kDecRows - 1) / kDecRows) * p.b.Hkv : 0;
+  d.tiles = max(1, (d.s.len + p.tile - 1) / p.tile);  // a sequence of no keys still gets its rows written
+  d.items = mine ? static_cast<int>((rows + p.rows - 1) / p.rows) * p.b.Hkv : 0;
   return d;
 }
 FA_HD long long decode_units(const DecodeParams& p, const DecodeSeq& d) {
@@ -245,64 +252,71 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // Octet position of key (or chunk) n: 0,4,1,5,2,6,3,7.
 __device__ __forceinline__ int spread8(int n) { return ((n & 1) << 2) | (n >> 1); }
 
-// One item's running state in one warp.  o[j]: accumulator of output column tile j; rows g and g + 8.
-template <int D>
+// 8 x 8 halves (or bf16) transposed across the warp: lane 4i + j gives row i, columns 2j and 2j + 1.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// One item's running state in one warp, query rows 8 n + 2t and 8 n + 2t + 1 of lane quarter t.
+template <int D, int NT>
 struct DecodeAcc {
-  float o[D / 8][4];
-  float m[2], l[2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
 };
 
-// Output column of element e (0, 1) of column tile j in lane quarter t.
-template <int D, bool FP8>
-__device__ __forceinline__ int out_col(int j, int t, int e) {
-  if constexpr (!FP8) return 8 * j + 2 * t + e;
-  constexpr int RUN = D / 8;  // columns that one lane's chunk of a value row holds
-  return RUN * (t + 4 * e) + j;
+// Warp `gives`'s state into warp `takes`'s (both hold the same rows and columns), eight query rows at a
+// time through `box`; every consumer warp calls it.
+template <int D, int NT>
+__device__ __forceinline__ void meet(DecodeAcc<D, NT>& a, uint8_t* box, int lane, bool gives, bool takes) {
+  constexpr int N = D / 16;
+  float4* f = reinterpret_cast<float4*>(box);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (gives) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j * 32 + lane] = make_float4(a.o[n][j][0], a.o[n][j][1], a.o[n][j][2], a.o[n][j][3]);
+      f[N * 32 + lane] = make_float4(a.m[n][0], a.l[n][0], a.m[n][1], a.l[n][1]);
+    }
+    named_barrier(1, 128);
+    if (takes) {
+      const float4 ml = f[N * 32 + lane];
+      const float mb[2] = {ml.x, ml.z}, lb[2] = {ml.y, ml.w};
+      float ca[2], cb[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mx = fmaxf(a.m[n][e], mb[e]);
+        const float ms = mx == -INFINITY ? 0.0f : mx;
+        ca[e] = exp2_sfu(a.m[n][e] - ms);
+        cb[e] = exp2_sfu(mb[e] - ms);
+        a.l[n][e] = a.l[n][e] * ca[e] + lb[e] * cb[e];
+        a.m[n][e] = mx;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float4 v = f[j * 32 + lane];
+        float* o = a.o[n][j];
+        o[0] = o[0] * ca[0] + v.x * cb[0];
+        o[1] = o[1] * ca[1] + v.y * cb[1];
+        o[2] = o[2] * ca[0] + v.z * cb[0];
+        o[3] = o[3] * ca[1] + v.w * cb[1];
+      }
+    }
+    named_barrier(1, 128);
+  }
 }
 
-// The other's state into this one's (both hold the same rows and columns).
-template <int D>
-__device__ __forceinline__ void absorb(DecodeAcc<D>& a, const uint8_t* from, int lane) {
-  const float4* f = reinterpret_cast<const float4*>(from);
-  const float4 ml = f[(D / 8) * 32 + lane];
-  float ca[2], cb[2];
-  const float mb[2] = {ml.x, ml.z}, lb[2] = {ml.y, ml.w};
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const float mx = fmaxf(a.m[r], mb[r]);
-    const float ms = mx == -INFINITY ? 0.0f : mx;
-    ca[r] = exp2f(a.m[r] - ms);
-    cb[r] = exp2f(mb[r] - ms);
-    a.l[r] = a.l[r] * ca[r] + lb[r] * cb[r];
-    a.m[r] = mx;
-  }
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    const float4 v = f[j * 32 + lane];
-    a.o[j][0] = a.o[j][0] * ca[0] + v.x * cb[0];
-    a.o[j][1] = a.o[j][1] * ca[0] + v.y * cb[0];
-    a.o[j][2] = a.o[j][2] * ca[1] + v.z * cb[1];
-    a.o[j][3] = a.o[j][3] * ca[1] + v.w * cb[1];
-  }
-}
-template <int D>
-__device__ __forceinline__ void leave(const DecodeAcc<D>& a, uint8_t* to, int lane) {
-  float4* f = reinterpret_cast<float4*>(to);
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j) f[j * 32 + lane] = make_float4(a.o[j][0], a.o[j][1], a.o[j][2], a.o[j][3]);
-  f[(D / 8) * 32 + lane] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
-}
-
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kDecThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecodeParams prm) {
   using L = DecodeLayout<D, FP8>;
-  constexpr int S = L::kStages, KS = D / 16, NJ = D / 8;
+  constexpr int S = L::kStages, KS = D / 16, NJ = D / 16, TILE = L::kTile, NS = TILE / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* empty = full + S;
-  float2* meta = reinterpret_cast<float2*>(smem + L::kMeta);
+  float4* meta = reinterpret_cast<float4*>(smem + L::kMeta);
   int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc);
   long long* scratch = reinterpret_cast<long long*>(smem + L::kMisc + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,8 +338,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const Guard g{abort_flag, prm.b.status};
   DecodeWalk w;
   w.start(prm, share, blockIdx.x);
-  const int box_rows = min(1 << prm.b.page_shift, kDecTile);
-  const int box_shift = min(prm.b.page_shift, 6);
+  const int box_shift = min(prm.b.page_shift, FP8 ? 7 : 6), box_rows = 1 << box_shift;
   int it = 0;  // tiles since the start: stage it % S
 
   if (warp == 4) {
@@ -338,37 +351,42 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       const int n_pages = (w.d.s.len + (1 << prm.b.page_shift) - 1) >> prm.b.page_shift;
       int held = -1;  // the 32 pages whose numbers and scales the lanes hold
       int page = -1;
-      float2 sc = make_float2(1.0f, 1.0f);
+      float4 sc = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
       for (int tile = w.t0; tile < w.t1; ++tile, ++it) {
-        const int keys = min(kDecTile, w.d.s.len - tile * kDecTile);  // <= 0: a sequence of no keys
+        const int keys = min(TILE, w.d.s.len - tile * TILE);  // <= 0: a sequence of no keys
         if (keys <= 0) {
           --it;
           continue;
         }
         const int boxes = (keys + box_rows - 1) >> box_shift;
-        const int first_page = (tile * kDecTile) >> prm.b.page_shift;
+        const int first_page = (tile * TILE) >> prm.b.page_shift;
         if ((first_page >> 5) != held) {  // a tile's pages lie in one aligned run of 32
           held = first_page >> 5;
           const int i = held * 32 + lane;
           page = i < n_pages ? load_page(prm.b, w.b, i) : -1;
           if (FP8 && page >= 0) {
             const size_t at = static_cast<size_t>(page) * prm.b.Hkv + h;
-            sc = make_float2(prm.Ks[at], fmaxf(prm.Vs[at], kScaleFloor));
+            const float vs = fmaxf(prm.Vs[at], kScaleFloor);
+            sc = make_float4(prm.Ks[at], log2f(vs), 1.0f / vs, 0.0f);
           }
         }
         const int my_page = __shfl_sync(0xffffffffu, page, (first_page + lane) & 31);
-        const float2 my_sc = make_float2(__shfl_sync(0xffffffffu, sc.x, (first_page + lane) & 31),
-                                         __shfl_sync(0xffffffffu, sc.y, (first_page + lane) & 31));
+        float4 my_sc = sc;
+        if constexpr (FP8) {
+          my_sc.x = __shfl_sync(0xffffffffu, sc.x, (first_page + lane) & 31);
+          my_sc.y = __shfl_sync(0xffffffffu, sc.y, (first_page + lane) & 31);
+          my_sc.z = __shfl_sync(0xffffffffu, sc.z, (first_page + lane) & 31);
+        }
         const int st = it % S;
         if (!(ok = wait_warp(&empty[st], ((it / S) & 1) ^ 1, g, kSiteDecode | 1))) break;
-        if (FP8 && lane < boxes) meta[st * 4 + lane] = my_sc;
+        if (FP8 && lane < boxes) meta[st * L::kBoxes + lane] = my_sc;
         __syncwarp();
         if (lane == 0) mbar_expect_tx(&full[st], 2 * boxes * box_rows * L::kRowBytes);
         __syncwarp();
         if (lane < boxes) {
           // a page out of range reads as zeros beyond the map's last head
           const int z = my_page >= 0 ? my_page * prm.b.Hkv + h : prm.b.num_pages * prm.b.Hkv;
-          const int y = (tile * kDecTile) & ((1 << prm.b.page_shift) - 1);
+          const int y = (tile * TILE) & ((1 << prm.b.page_shift) - 1);
           constexpr int kCols = FP8 ? D : 64;
 #pragma unroll
           for (int c = 0; c < D / kCols; ++c) {
@@ -393,72 +411,72 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   bool ok = true;
   do {
     const int h = w.item % prm.b.Hkv, rb = w.item / prm.b.Hkv;
-    const int rows = w.d.s.rows * prm.G - rb * kDecRows;  // real rows of the block
+    const int rows = w.d.s.rows * prm.G - rb * (8 * NT);  // real rows of the block
     const int len = w.d.s.len;
-    // this lane's rows: query pointers, last visible key, score factor
-    uint32_t qf[KS][4];
-    float rowfac[2];
-    int lim[2];
-    float amax[2] = {0.0f, 0.0f};
-    const __nv_bfloat16* qrow[2];
+    // Q: row 8 n + gid; what the scores need of rows 8 n + 2t + e: last visible key, factor
+    uint32_t qf[NT][KS][2];
+    float rowfac[NT][2];
+    int lim[NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = rb * kDecRows + gid + 8 * r;
-      const bool real = gid + 8 * r < rows;
-      const int token = real ? row / prm.G : 0, head = h * prm.G + (real ? row % prm.G : 0);
-      qrow[r] = real ? prm.Q + static_cast<size_t>(w.d.s.row0 + token) * prm.ldq + head * D : nullptr;
-      lim[r] = prm.causal && real ? len - w.d.s.rows + token : len - 1;
-      rowfac[r] = prm.scale_log2;
-    }
-    if constexpr (FP8) {
-      uint2 qw[2][KS];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int n = 0; n < NT; ++n) {
+      const int row = rb * (8 * NT) + 8 * n + gid;
+      const __nv_bfloat16* q = nullptr;
+      if (8 * n + gid < rows)
+        q = prm.Q + static_cast<size_t>(w.d.s.row0 + row / prm.G) * prm.ldq + (h * prm.G + row % prm.G) * D;
+      if constexpr (FP8) {
+        uint2 qw[KS];
+        float amax = 0.0f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           const int col = 16 * (t + 4 * (s >> 2)) + (s & 3) * 4;
-          qw[r][s] = qrow[r] ? *reinterpret_cast<const uint2*>(qrow[r] + col) : make_uint2(0u, 0u);
-          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[r][s].x));
-          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[r][s].y));
-          amax[r] = fmaxf(fmaxf(amax[r], fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+          qw[s] = q ? *reinterpret_cast<const uint2*>(q + col) : make_uint2(0u, 0u);
+          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[s].x));
+          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[s].y));
+          amax = fmaxf(fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
         }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        amax[r] = fmaxf(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 1));
-        amax[r] = fmaxf(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 2));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // a power of two above the row's largest magnitude (kept where its inverse is normal)
-        const int e = min(max(static_cast<int>(__float_as_uint(amax[r]) >> 23) + 1, 2), 252);
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 2), 252);
         const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
         const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        rowfac[r] = prm.scale_log2 * up;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[r][s].x));
-          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[r][s].y));
-          qf[s][r] = pack_half2(a.x * down, a.y * down);
-          qf[s][2 + r] = pack_half2(b.x * down, b.y * down);
+          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[s].x));
+          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qw[s].y));
+          qf[n][s][0] = pack_half2(a.x * down, a.y * down);
+          qf[n][s][1] = pack_half2(b.x * down, b.y * down);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          rowfac[n][i] = prm.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + i) * 4);
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          qf[n][s][0] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t) : 0u;
+          qf[n][s][1] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t + 8) : 0u;
+        }
+        rowfac[n][0] = rowfac[n][1] = prm.scale_log2;
       }
-    } else {
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const __nv_bfloat16* q = qrow[r] ? qrow[r] + 16 * s + 2 * t : nullptr;
-          qf[s][r] = q ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-          qf[s][2 + r] = q ? *reinterpret_cast<const uint32_t*>(q + 8) : 0u;
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int lr = 8 * n + 2 * t + e;
+        lim[n][e] = prm.causal && lr < rows ? len - w.d.s.rows + (rb * (8 * NT) + lr) / prm.G : len - 1;
+      }
     }
-    const int lim_min = prm.causal ? len - w.d.s.rows + rb * kDecRows / prm.G : len - 1;
-    DecodeAcc<D> acc;
+    const int lim_min = prm.causal ? len - w.d.s.rows + rb * (8 * NT) / prm.G : len - 1;
+    DecodeAcc<D, NT> acc;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc.o[j][0] = acc.o[j][1] = acc.o[j][2] = acc.o[j][3] = 0.0f;
-    acc.m[0] = acc.m[1] = -INFINITY;
-    acc.l[0] = acc.l[1] = 0.0f;
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc.o[n][j][0] = acc.o[n][j][1] = acc.o[n][j][2] = acc.o[n][j][3] = 0.0f;
+      acc.m[n][0] = acc.m[n][1] = -INFINITY;
+      acc.l[n][0] = acc.l[n][1] = 0.0f;
+    }
 
     for (int tile = w.t0; tile < w.t1; ++tile, ++it) {
-      const int key0 = tile * kDecTile + warp * 16;
-      if (tile * kDecTile >= len) {
+      const int row0 = warp * (16 * NS), key0 = tile * TILE + row0;  // this warp's first row of the tile
+      if (tile * TILE >= len) {
         --it;
         continue;
       }
@@ -466,221 +484,265 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       if (!(ok = wait_warp(&full[st], (it / S) & 1, g, kSiteDecode | 2))) break;
       if (key0 < len) {
         const uint32_t sK = smem_u32(smem + st * L::kTileBytes), sV = smem_u32(smem + L::kV + st * L::kTileBytes);
-        if (key0 + 16 > len) {
+        if (key0 + 16 * NS > len) {
           // slots behind the sequence's end hold whatever the page holds: their values become zeros, since
           // a weight of zero times an infinity or NaN is not zero
           constexpr int kCols = FP8 ? D : 128;  // bytes of a row in a column block
-          for (int i = lane; i < 16 * L::kRowBytes / 16; i += 32) {
-            const int row = warp * 16 + (i / (kCols / 16)) % 16, blk = i / (kCols / 16) / 16;
-            if (tile * kDecTile + row >= len)
+          for (int i = lane; i < NS * L::kRowBytes; i += 32) {
+            const int row = row0 + (i / (kCols / 16)) % (16 * NS), blk = i / (kCols / 16) / (16 * NS);
+            if (tile * TILE + row >= len)
               *reinterpret_cast<uint4*>(smem + L::kV + st * L::kTileBytes + blk * L::kHalf + row * kCols +
                                         (i % (kCols / 16)) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           __syncwarp();
         }
-        // ---- S = Q K^T: two octets of keys
-        float c[2][4];
+        // ---- S^T = K Q^T: 16 keys at a time; c[.][.][2r + e] is key (row of lane) + 8r, query row 2t + e
+        float c[NS][NT][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) c[s][n][0] = c[s][n][1] = c[s][n][2] = c[s][n][3] = 0.0f;
         if constexpr (FP8) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int row = warp * 16 + n * 8 + spread8(gid);
+          for (int cc = 0; cc < KS / 4; ++cc) {
 #pragma unroll
-            for (int cc = 0; cc < KS / 4; ++cc) {
-              const int chunk = t + 4 * cc;
-              const uint32_t a = D == 128 ? sK + row * 128 + ((chunk ^ (row & 7)) << 4)
-                                          : sK + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-              const uint4 v = lds128(a);
-              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            for (int s = 0; s < NS; ++s) {
+              uint32_t x[2][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma16816<FP8>(c[n], qf[cc * 4 + i], half2_of_e4m3(x[i]), half2_of_e4m3(x[i] >> 16));
+              for (int r = 0; r < 2; ++r) {
+                const int row = row0 + 16 * s + 8 * r + spread8(gid), chunk = t + 4 * cc;
+                const uint4 v = lds128(D == 128 ? sK + row * 128 + ((chunk ^ (row & 7)) << 4)
+                                                : sK + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+                x[r][0] = v.x, x[r][1] = v.y, x[r][2] = v.z, x[r][3] = v.w;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t a[4];
+                halves_of_e4m3(x[0][i], a[0], a[2]);
+                halves_of_e4m3(x[1][i], a[1], a[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<FP8>(c[s][n], a, qf[n][cc * 4 + i][0], qf[n][cc * 4 + i][1]);
+              }
             }
           }
         } else {
-          const int row = warp * 16 + (lane >> 4) * 8 + (lane & 7);
+          const int row = row0 + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            uint32_t kf[4];
-            const int chunk = (s & 3) * 2 + ((lane >> 3) & 1);
-            ldsm4(sK + (s >> 2) * L::kHalf + row * 128 + ((chunk ^ (row & 7)) << 4), kf);
-            mma16816<FP8>(c[0], qf[s], kf[0], kf[1]);
-            mma16816<FP8>(c[1], qf[s], kf[2], kf[3]);
+          for (int k = 0; k < KS; ++k) {
+            uint32_t a[4];
+            const int chunk = (k & 3) * 2 + (lane >> 4);
+            ldsm4(sK + (k >> 2) * L::kHalf + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<FP8>(c[0][n], a, qf[n][k][0], qf[n][k][1]);
           }
         }
         // ---- softmax: scores in log2 units (plus log2 of the value scale)
-        float ks = 1.0f, lv = 0.0f, inv_vs = 1.0f;
-        if constexpr (FP8) {
-          const float2 sc = meta[st * 4 + ((warp * 16) >> box_shift)];
-          ks = sc.x;
-          lv = log2f(sc.y);
-          inv_vs = 1.0f / sc.y;
-        }
-        const float f0 = rowfac[0] * ks, f1 = rowfac[1] * ks;
+        float inv_vs[NS];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          c[n][0] = fmaf(c[n][0], f0, lv);
-          c[n][1] = fmaf(c[n][1], f0, lv);
-          c[n][2] = fmaf(c[n][2], f1, lv);
-          c[n][3] = fmaf(c[n][3], f1, lv);
-        }
-        if (key0 + 15 > lim_min) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key0 + n * 8 + (FP8 ? t + 4 * (i & 1) : 2 * t + (i & 1));
-              if (key > lim[i >> 1]) c[n][i] = -INFINITY;
+        for (int s = 0; s < NS; ++s) {
+          float ks = 1.0f, lv = 0.0f;
+          inv_vs[s] = 1.0f;
+          if constexpr (FP8) {
+            if (s == 0 || key0 + 16 * s < len) {  // a page behind the end brought no scales
+              const float4 sc = meta[st * L::kBoxes + ((row0 + 16 * s) >> box_shift)];
+              ks = sc.x;
+              lv = sc.y;
+              inv_vs[s] = sc.z;
             }
-        }
-        float mx[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          mx[r] = fmaxf(fmaxf(c[0][2 * r], c[0][2 * r + 1]), fmaxf(c[1][2 * r], c[1][2 * r + 1]));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        }
-        if (__any_sync(0xffffffffu, mx[0] > acc.m[0] || mx[1] > acc.m[1])) {
-          float al[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float m = fmaxf(acc.m[r], mx[r]);
-            al[r] = m == -INFINITY ? 1.0f : exp2_sfu(acc.m[r] - m);
-            acc.m[r] = m;
-            acc.l[r] *= al[r];
           }
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            acc.o[j][0] *= al[0];
-            acc.o[j][1] *= al[0];
-            acc.o[j][2] *= al[1];
-            acc.o[j][3] *= al[1];
+          for (int n = 0; n < NT; ++n) {
+            const float f0 = rowfac[n][0] * ks, f1 = rowfac[n][1] * ks;
+            c[s][n][0] = fmaf(c[s][n][0], f0, lv);
+            c[s][n][1] = fmaf(c[s][n][1], f1, lv);
+            c[s][n][2] = fmaf(c[s][n][2], f0, lv);
+            c[s][n][3] = fmaf(c[s][n][3], f1, lv);
           }
         }
-        const float m0 = acc.m[0] == -INFINITY ? 0.0f : acc.m[0], m1 = acc.m[1] == -INFINITY ? 0.0f : acc.m[1];
-        float p[2][4];
+        if (key0 + 16 * NS - 1 > lim_min) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          p[n][0] = exp2_sfu(c[n][0] - m0);
-          p[n][1] = exp2_sfu(c[n][1] - m0);
-          p[n][2] = exp2_sfu(c[n][2] - m1);
-          p[n][3] = exp2_sfu(c[n][3] - m1);
-        }
-        acc.l[0] = fmaf(p[0][0] + p[0][1] + (p[1][0] + p[1][1]), inv_vs, acc.l[0]);
-        acc.l[1] = fmaf(p[0][2] + p[0][3] + (p[1][2] + p[1][3]), inv_vs, acc.l[1]);
-        uint32_t pf[4];
+          for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          pf[2 * n] = FP8 ? pack_half2(p[n][0], p[n][1]) : pack_bf16x2(p[n][0], p[n][1]);
-          pf[2 * n + 1] = FP8 ? pack_half2(p[n][2], p[n][3]) : pack_bf16x2(p[n][2], p[n][3]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key0 + 16 * s + 8 * (i >> 1) + (FP8 ? spread8(gid) : gid);
+                if (key > lim[n][i & 1]) c[s][n][i] = -INFINITY;
+              }
         }
-        // ---- O += P V
+        float mx[NT][2];
+        bool passed = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[n][e] = fmaxf(c[0][n][e], c[0][n][2 + e]);
+#pragma unroll
+            for (int s = 1; s < NS; ++s) mx[n][e] = fmax3(mx[n][e], c[s][n][e], c[s][n][2 + e]);
+            passed |= mx[n][e] > acc.m[n][e] + kDecTau;
+          }
+        if (__any_sync(0xffffffffu, passed)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float m = mx[n][e];
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              m = fmaxf(m, acc.m[n][e]);
+              al[e] = m == -INFINITY ? 1.0f : exp2_sfu(acc.m[n][e] - m);
+              acc.m[n][e] = m;
+              acc.l[n][e] *= al[e];
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              acc.o[n][j][0] *= al[0];
+              acc.o[n][j][1] *= al[1];
+              acc.o[n][j][2] *= al[0];
+              acc.o[n][j][3] *= al[1];
+            }
+          }
+        }
+        uint32_t pf[NS][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = acc.m[n][0] == -INFINITY ? 0.0f : acc.m[n][0];
+          const float m1 = acc.m[n][1] == -INFINITY ? 0.0f : acc.m[n][1];
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const float p0 = exp2_sfu(c[s][n][0] - m0), p1 = exp2_sfu(c[s][n][1] - m1);
+            const float p2 = exp2_sfu(c[s][n][2] - m0), p3 = exp2_sfu(c[s][n][3] - m1);
+            acc.l[n][0] = FP8 ? fmaf(p0 + p2, inv_vs[s], acc.l[n][0]) : acc.l[n][0] + (p0 + p2);
+            acc.l[n][1] = FP8 ? fmaf(p1 + p3, inv_vs[s], acc.l[n][1]) : acc.l[n][1] + (p1 + p3);
+            pf[s][n][0] = transpose8x8(FP8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1));
+            pf[s][n][1] = transpose8x8(FP8 ? pack_half2(p2, p3) : pack_bf16x2(p2, p3));
+          }
+        }
+        // ---- O^T += V^T P^T
         if constexpr (FP8) {
           constexpr int WORDS = D / 32;  // 4-byte words of a lane's chunk of a value row
-          uint32_t v[4][WORDS];
           const int chunk = spread8(gid);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = warp * 16 + t + 4 * i;
-            if constexpr (D == 128) {
-              const uint4 x = lds128(sV + row * 128 + ((chunk ^ (row & 7)) << 4));
-              v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-            } else {
-              const uint2 x = lds64(sV + row * 64 + (((chunk >> 1) ^ ((row >> 1) & 3)) << 4) + (chunk & 1) * 8);
-              v[i][0] = x.x, v[i][1] = x.y;
+          for (int s = 0; s < NS; ++s) {
+            uint32_t v[4][WORDS];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = row0 + 16 * s + t + 4 * i;
+              if constexpr (D == 128) {
+                const uint4 x = lds128(sV + row * 128 + ((chunk ^ (row & 7)) << 4));
+                v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+              } else {
+                const uint2 x = lds64(sV + row * 64 + (((chunk >> 1) ^ ((row >> 1) & 3)) << 4) + (chunk & 1) * 8);
+                v[i][0] = x.x, v[i][1] = x.y;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+              // bytes of two keys interleaved: columns 4i (row gid of the tile) and 4i + 1 (row gid + 8), then two more
+              uint32_t a[2][4];
+              halves_of_e4m3(__byte_perm(v[0][i], v[1][i], 0x5140), a[0][0], a[0][1]);
+              halves_of_e4m3(__byte_perm(v[2][i], v[3][i], 0x5140), a[0][2], a[0][3]);
+              halves_of_e4m3(__byte_perm(v[0][i], v[1][i], 0x7362), a[1][0], a[1][1]);
+              halves_of_e4m3(__byte_perm(v[2][i], v[3][i], 0x7362), a[1][2], a[1][3]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<FP8>(acc.o[n][2 * i + e], a[e], pf[s][n][0], pf[s][n][1]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < WORDS; ++i) {
-            // bytes of two keys interleaved: column 4i in the low half, 4i + 1 in the high one; then 4i + 2, 4i + 3
-            const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5140), a1 = __byte_perm(v[0][i], v[1][i], 0x7362);
-            const uint32_t b0 = __byte_perm(v[2][i], v[3][i], 0x5140), b1 = __byte_perm(v[2][i], v[3][i], 0x7362);
-            mma16816<FP8>(acc.o[4 * i], pf, half2_of_e4m3(a0), half2_of_e4m3(b0));
-            mma16816<FP8>(acc.o[4 * i + 1], pf, half2_of_e4m3(a0 >> 16), half2_of_e4m3(b0 >> 16));
-            mma16816<FP8>(acc.o[4 * i + 2], pf, half2_of_e4m3(a1), half2_of_e4m3(b1));
-            mma16816<FP8>(acc.o[4 * i + 3], pf, half2_of_e4m3(a1 >> 16), half2_of_e4m3(b1 >> 16));
-          }
         } else {
-          const int row = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+          const int row = row0 + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
-          for (int j = 0; j < NJ; j += 2) {
-            uint32_t vf[4];
-            const int chunk = (j & 7) + (lane >> 4);
-            ldsm4_t(sV + (j >> 3) * L::kHalf + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
-            mma16816<FP8>(acc.o[j], pf, vf[0], vf[1]);
-            mma16816<FP8>(acc.o[j + 1], pf, vf[2], vf[3]);
+          for (int j = 0; j < NJ; ++j) {
+            uint32_t a[4];
+            const int chunk = (2 * j & 7) + ((lane >> 3) & 1);
+            ldsm4_t(sV + (j >> 2) * L::kHalf + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<FP8>(acc.o[n][j], a, pf[0][n][0], pf[0][n][1]);
           }
         }
         // zeros written above must be done before TMA writes the stage again
-        if (key0 + 16 > len) fence_proxy_async();
+        if (key0 + 16 * NS > len) fence_proxy_async();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
 
-    // ---- the four warps meet: 2 and 3 into 0 and 1, then 1 into 0
+    // ---- the lanes of a row add up, then the four warps meet: 2 and 3 into 0 and 1, then 1 into 0
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], 1);
-      acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], 2);
-    }
-    uint8_t* box = smem + L::kMerge + (warp & 1) * L::kMergeWarp;
-    if (warp >= 2) leave<D>(acc, box, lane);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) acc.l[n][e] += __shfl_xor_sync(0xffffffffu, acc.l[n][e], o);
     if (!(ok = group_and(1, 128, ok))) break;
-    if (warp < 2) absorb<D>(acc, box, lane);
-    named_barrier(1, 128);
-    if (warp == 1) leave<D>(acc, box, lane);
-    named_barrier(1, 128);
+    meet<D, NT>(acc, smem + L::kMerge + (warp & 1) * L::kMergeWarp, lane, warp >= 2, warp < 2);
+    meet<D, NT>(acc, smem + L::kMerge, lane, warp == 1, warp == 0);
     if (warp == 0) {
-      absorb<D>(acc, smem + L::kMerge + L::kMergeWarp, lane);
-      const int slot = decode_slot(blockIdx.x, w.t0);
+      const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, w.t0)) * prm.rows;
+      constexpr int RUN = D / 8;  // e4m3: consecutive columns of a lane, from RUN * spread8(gid)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int lr = gid + 8 * r;
-        if (lr >= rows) continue;
-        const float scale = !w.whole ? 1.0f : acc.l[r] > 0.0f ? 1.0f / acc.l[r] : 0.0f;
-        float x[NJ][2];
+      for (int n = 0; n < NT; ++n) {
+        if constexpr (FP8) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) x[j][0] = acc.o[j][2 * r] * scale, x[j][1] = acc.o[j][2 * r + 1] * scale;
-        if (w.whole) {
-          const int row = rb * kDecRows + lr;
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * n + 2 * t + e, row = rb * (8 * NT) + lr;
+            if (lr >= rows) continue;
+            float x[RUN];
+            const float scale = !w.whole ? 1.0f : acc.l[n][e] > 0.0f ? 1.0f / acc.l[n][e] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) x[2 * j] = acc.o[n][j][e] * scale, x[2 * j + 1] = acc.o[n][j][2 + e] * scale;
+            if (w.whole) {
+              const size_t at = static_cast<size_t>(w.d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G;
+#pragma unroll
+              for (int j = 0; j < RUN; j += 8)
+                *reinterpret_cast<uint4*>(prm.O + at * D + RUN * spread8(gid) + j) =
+                    make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]),
+                               pack_bf16x2(x[j + 4], x[j + 5]), pack_bf16x2(x[j + 6], x[j + 7]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < RUN; j += 4)
+                *reinterpret_cast<float4*>(prm.part_o + (slot + lr) * D + RUN * spread8(gid) + j) =
+                    make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            }
+          }
+        } else if (w.whole) {
+          // two rows' values of one column become two columns of one row, so that a lane stores pairs
+          const float i0 = acc.l[n][0] > 0.0f ? 1.0f / acc.l[n][0] : 0.0f;
+          const float i1 = acc.l[n][1] > 0.0f ? 1.0f / acc.l[n][1] : 0.0f;
+          const int row = rb * (8 * NT) + 8 * n + gid;
           const size_t at = static_cast<size_t>(w.d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G;
-          __nv_bfloat16* o = prm.O + at * D;
-          if constexpr (FP8) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int j = 0; j < NJ; j += 8)
-                *reinterpret_cast<uint4*>(o + out_col<D, FP8>(j, t, e)) =
-                    make_uint4(pack_bf16x2(x[j][e], x[j + 1][e]), pack_bf16x2(x[j + 2][e], x[j + 3][e]),
-                               pack_bf16x2(x[j + 4][e], x[j + 5][e]), pack_bf16x2(x[j + 6][e], x[j + 7][e]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-              *reinterpret_cast<uint32_t*>(o + out_col<D, FP8>(j, t, 0)) = pack_bf16x2(x[j][0], x[j][1]);
+          for (int j = 0; j < 2 * NJ; ++j) {
+            const float* o = acc.o[n][j >> 1] + 2 * (j & 1);
+            const uint32_t y = transpose8x8(pack_bf16x2(o[0] * i0, o[1] * i1));
+            if (8 * n + gid < rows) *reinterpret_cast<uint32_t*>(prm.O + at * D + 8 * j + 2 * t) = y;
           }
-          if (t == 0)
-            prm.LSE[at] = acc.l[r] > 0.0f ? (acc.m[r] + log2f(acc.l[r])) * 0.69314718055994531f : -INFINITY;
         } else {
-          float* o = prm.part_o + (static_cast<size_t>(slot) * kDecRows + lr) * D;
-          if constexpr (FP8) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * n + 2 * t + e;
+            if (lr >= rows) continue;
 #pragma unroll
-              for (int j = 0; j < NJ; j += 4)
-                *reinterpret_cast<float4*>(o + out_col<D, FP8>(j, t, e)) =
-                    make_float4(x[j][e], x[j + 1][e], x[j + 2][e], x[j + 3][e]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-              *reinterpret_cast<float2*>(o + out_col<D, FP8>(j, t, 0)) = make_float2(x[j][0], x[j][1]);
+            for (int j = 0; j < 2 * NJ; ++j)
+              prm.part_o[(slot + lr) * D + 8 * j + gid] = acc.o[n][j >> 1][2 * (j & 1) + e];
           }
-          if (t == 0) prm.part_ml[static_cast<size_t>(slot) * kDecRows + lr] = make_float2(acc.m[r], acc.l[r]);
         }
+        if (gid == 0)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * n + 2 * t + e, row = rb * (8 * NT) + lr;
+            if (lr >= rows) continue;
+            if (w.whole)
+              prm.LSE[static_cast<size_t>(w.d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G] =
+                  acc.l[n][e] > 0.0f ? (acc.m[n][e] + log2f(acc.l[n][e])) * 0.69314718055994531f : -INFINITY;
+            else
+              prm.part_ml[slot + lr] = make_float2(acc.m[n][e], acc.l[n][e]);
+          }
       }
     }
-    named_barrier(1, 128);  // the merge area is free again
   } while (w.next(prm));
 }
 
@@ -699,8 +761,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
   if (cut.last < c || cut.first != c - 1) return;
   const int item = cut.item, last = cut.last;
   const int h = item % prm.b.Hkv, rb = item / prm.b.Hkv;
-  const int rows = min(kDecRows, d.s.rows * prm.G - rb * kDecRows);
-  auto slot = [&](int cta) { return static_cast<size_t>(decode_slot(cta, cta - (c - 1))) * kDecRows; };
+  const int rows = min(prm.rows, d.s.rows * prm.G - rb * prm.rows);
+  auto slot = [&](int cta) { return static_cast<size_t>(decode_slot(cta, cta - (c - 1))) * prm.rows; };
   for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
     const int lr = i / (D / 4), col = (i % (D / 4)) * 4;
     float m = -INFINITY;
@@ -720,7 +782,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
       o.w = fmaf(f, v.w, o.w);
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int row = rb * kDecRows + lr;
+    const int row = rb * prm.rows + lr;
     const size_t at = static_cast<size_t>(d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G;
     *reinterpret_cast<uint2*>(prm.O + at * D + col) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));

@@ -72,6 +72,8 @@ static void shares(std::mt19937& rng, bool whole) {
   p.b.Hkv = pick(1, 4);
   p.b.status = &status;
   p.G = pick(1, 5);
+  p.tile = pick(0, 1) ? 64 : 128;
+  p.rows = pick(0, 1) ? 8 : 16;
   p.max_rows = pick(0, 2) ? 1 << 30 : 48;
   p.whole = whole;
   long long total = 0;
