@@ -24,6 +24,11 @@ enum : int {
   kBadPosition = kSitePaged | 4,  // a position beyond the rotation's tables
 };
 
+// The next kernel of the stream, if it was launched to overlap with this one, may be scheduled from here on.
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits for the kernel before, if this one was launched to overlap with it, to end, its writes visible.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct PagedBatch {
   const int* table;  // [B, max_pages]
   const int* cu_q;   // [B + 1]

@@ -12,6 +12,8 @@
 #include "fa_host.h"
 #include "fa_paged.cuh"
 #include "fa_paged_decode.cuh"
+#include "fa_paged_join.cuh"
+#include "fa_paged_prefill.cuh"
 
 using namespace fa_host;
 
@@ -20,6 +22,9 @@ namespace {
 // Short caches (at most this many keys by the block table's width) are not cut along the keys: each CTA
 // takes whole items and nothing is joined.
 constexpr int kWholeKeys = 256;
+// Sequences of at most this many rows (new tokens x query heads of a key/value head) go to the kernel of few
+// rows, longer ones to the tensor-core tiles.
+constexpr int kDecodeMaxRows = 32;
 
 struct Sizes {
   size_t cache, scales, table;
@@ -122,46 +127,78 @@ int launch_append(const fa::AppendParams& prm, long long grid, cudaStream_t st) 
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct PagedWs {
-  size_t o, ml, total;
+  size_t dec_o, dec_ml, pre_o, pre_ml, total;
 };
-PagedWs paged_ws(int d, int n_cta) {
+// The kernel of many rows has its parts only where a sequence may have as many.
+PagedWs paged_ws(int d, bool many) {
   PagedWs w;
-  w.o = 0;
-  w.ml = round256(static_cast<size_t>(2) * n_cta * fa::kDecRows * d * 4);
-  w.total = w.ml + round256(static_cast<size_t>(2) * n_cta * fa::kDecRows * 8);
+  w.dec_o = 0;
+  w.dec_ml = round256(static_cast<size_t>(2) * fa::kDecCtas * fa::kDecRows * d * 4);
+  w.pre_o = w.dec_ml + round256(static_cast<size_t>(2) * fa::kDecCtas * fa::kDecRows * 8);
+  w.pre_ml = w.pre_o + (many ? round256(static_cast<size_t>(2) * fa::kPreCtas * fa::kPreRows * d * 4) : 0);
+  w.total = w.pre_ml + (many ? round256(static_cast<size_t>(2) * fa::kPreCtas * fa::kPreRows * 8) : 0);
   return w;
+}
+bool many_rows(const fa_paged_batch* b, int T, int G) {
+  return static_cast<long long>(b->max_q < T ? b->max_q : T) * G > kDecodeMaxRows;
 }
 bool whole_items(const fa_paged_cache* c, const fa_paged_batch* b) {
   return static_cast<long long>(b->max_pages) * c->page_size <= kWholeKeys;
 }
 
-template <int D, bool FP8, int NT>
-int launch_decode(const CUtensorMap& k, const CUtensorMap& v, const fa::DecodeParams& prm, int n_cta, cudaStream_t st) {
-  using L = fa::DecodeLayout<D, FP8>;
-  auto kern = fa::decode_kernel<D, FP8, NT>;
-  if (set_smem(kern, L::kBytes) != cudaSuccess) return FA_ERR_CUDA;
-  kern<<<n_cta, fa::kDecThreads, L::kBytes, st>>>(k, v, prm);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (prm.whole || n_cta == 1) return FA_OK;
-  // the join may be scheduled while the shares run; it waits for them before it reads
+struct FwdMaps {
+  CUtensorMap dec_k, dec_v, pre_k, pre_v;
+};
+
+// A launch that may be scheduled while the stream's kernel before it still runs.
+template <typename... P>
+bool launch_overlapped(void (*kern)(P...), int grid, int threads, int smem, cudaStream_t st, const P&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_cta - 1);
-  cfg.blockDim = dim3(fa::kJoinThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa::decode_join_kernel<D>, prm, n_cta) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
 }
 
+template <int D, bool FP8, int NT>
+int launch_fwd_paged(const FwdMaps& m, const fa::DecodeParams& dec, const fa::PrefillParams& pre, bool many,
+                     cudaStream_t st) {
+  using LD = fa::DecodeLayout<D, FP8>;
+  using LP = fa::PrefillLayout<D, FP8>;
+  auto dkern = fa::decode_kernel<D, FP8, NT>;
+  auto pkern = fa::prefill_kernel<D, FP8>;
+  if (set_smem(dkern, LD::kBytes) != cudaSuccess) return FA_ERR_CUDA;
+  if (many) {
+    if (set_smem(pkern, LP::kBytes) != cudaSuccess) return FA_ERR_CUDA;
+    pkern<<<fa::kPreCtas, LP::kThreads, LP::kBytes, st>>>(m.pre_k, m.pre_v, pre);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    // the two share no data: the few rows' blocks fill SMs as the many rows' ones leave them
+    if (!launch_overlapped(dkern, fa::kDecCtas, fa::kDecThreads, LD::kBytes, st, m.dec_k, m.dec_v, dec)) return FA_ERR_CUDA;
+  } else {
+    dkern<<<fa::kDecCtas, fa::kDecThreads, LD::kBytes, st>>>(m.dec_k, m.dec_v, dec);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  const int dec_cuts = dec.whole ? 0 : fa::kDecCtas - 1, pre_cuts = many ? fa::kPreCtas - 1 : 0;
+  if (dec_cuts + pre_cuts == 0) return FA_OK;
+  return launch_overlapped(fa::join_kernel<D>, dec_cuts + pre_cuts * fa::kJoinSplit, fa::kJoinThreads, 0, st, dec, pre,
+                           dec_cuts + 1)
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
 template <int NT>
-int launch_decode_type(int d, bool fp8, const CUtensorMap& k, const CUtensorMap& v, const fa::DecodeParams& prm,
-                       int n_cta, cudaStream_t st) {
+int launch_fwd_paged_type(int d, bool fp8, const FwdMaps& m, const fa::DecodeParams& dec, const fa::PrefillParams& pre,
+                          bool many, cudaStream_t st) {
   if (d == 128)
-    return fp8 ? launch_decode<128, true, NT>(k, v, prm, n_cta, st) : launch_decode<128, false, NT>(k, v, prm, n_cta, st);
-  return fp8 ? launch_decode<64, true, NT>(k, v, prm, n_cta, st) : launch_decode<64, false, NT>(k, v, prm, n_cta, st);
+    return fp8 ? launch_fwd_paged<128, true, NT>(m, dec, pre, many, st)
+               : launch_fwd_paged<128, false, NT>(m, dec, pre, many, st);
+  return fp8 ? launch_fwd_paged<64, true, NT>(m, dec, pre, many, st)
+             : launch_fwd_paged<64, false, NT>(m, dec, pre, many, st);
 }
 
 }  // namespace
@@ -240,7 +277,7 @@ size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_b
   bool empty = false;
   Sizes z;
   if (check_paged(cache, batch, T, Hq, true, &empty, &z) != FA_OK || empty) return 0;
-  return paged_ws(cache->d, fa::kDecCtas).total;
+  return paged_ws(cache->d, many_rows(batch, T, Hq / cache->heads)).total;
 }
 
 int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const fa_paged_batch* batch, int T, void* O,
@@ -255,8 +292,9 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   if (ldq < static_cast<int64_t>(Hq) * cache->d) return FA_ERR_INVALID_ARG;
   if (ldq % 8 || !aligned16(Q) || !aligned16(O) || !aligned16(LSE) || !aligned16(workspace)) return FA_ERR_ALIGNMENT;
   if (ldq > (1LL << 40) / T || static_cast<long long>(T) * Hq > INT_MAX) return FA_ERR_UNSUPPORTED;
-  const int n_cta = fa::kDecCtas;
-  const PagedWs ws = paged_ws(cache->d, n_cta);
+  const int G = Hq / cache->heads;
+  const bool many = many_rows(batch, T, G);
+  const PagedWs ws = paged_ws(cache->d, many);
   if (workspace_bytes < ws.total) return FA_ERR_INVALID_ARG;
   const size_t qb = rows_bytes(T, ldq, Hq, cache->d), ob = static_cast<size_t>(T) * Hq * cache->d * 2;
   const size_t lb = static_cast<size_t>(T) * Hq * 4;
@@ -271,30 +309,50 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   if (!status) return rc;
   const bool fp8 = cache->type == FA_CACHE_E4M3;
   const int tile = fp8 ? fa::DecodeLayout<128, true>::kTile : fa::DecodeLayout<128, false>::kTile;
+  FwdMaps m;
   const int box = cache->page_size < tile ? cache->page_size : tile;
-  CUtensorMap mk, mv;
-  if (!make_page_map(&mk, cache->K, cache, box) || !make_page_map(&mv, cache->V, cache, box)) return FA_ERR_CUDA;
-  fa::DecodeParams prm;
-  prm.b = device_batch(cache, batch, T, status);
-  prm.Q = static_cast<const __nv_bfloat16*>(Q);
-  prm.ldq = ldq;
-  prm.O = static_cast<__nv_bfloat16*>(O);
-  prm.LSE = LSE;
-  prm.Ks = cache->K_scale;
-  prm.Vs = cache->V_scale;
-  prm.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.o);
-  prm.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ml);
-  prm.G = Hq / cache->heads;
-  prm.Hq = Hq;
-  prm.tile = tile;
-  prm.rows = static_cast<long long>(batch->max_q) * prm.G <= 8 ? 8 : 16;
-  prm.max_rows = INT_MAX;
-  prm.causal = causal;
-  prm.whole = whole_items(cache, batch) ? 1 : 0;
-  prm.scale_log2 = scale * 1.4426950408889634f;
+  if (!make_page_map(&m.dec_k, cache->K, cache, box) || !make_page_map(&m.dec_v, cache->V, cache, box) ||
+      !make_page_map(&m.pre_k, cache->K, cache, cache->page_size) ||
+      !make_page_map(&m.pre_v, cache->V, cache, cache->page_size))
+    return FA_ERR_CUDA;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  fa::DecodeParams dec;
+  dec.b = device_batch(cache, batch, T, status);
+  dec.Q = static_cast<const __nv_bfloat16*>(Q);
+  dec.ldq = ldq;
+  dec.O = static_cast<__nv_bfloat16*>(O);
+  dec.LSE = LSE;
+  dec.Ks = cache->K_scale;
+  dec.Vs = cache->V_scale;
+  dec.part_o = reinterpret_cast<float*>(wsb + ws.dec_o);
+  dec.part_ml = reinterpret_cast<float2*>(wsb + ws.dec_ml);
+  dec.G = G;
+  dec.Hq = Hq;
+  dec.tile = tile;
+  // eight rows an item where single tokens fit them and are most of what comes; sixteen for a few tokens
+  dec.rows = G <= 8 && (many || static_cast<long long>(batch->max_q) * G <= 8) ? 8 : 16;
+  dec.max_rows = kDecodeMaxRows;
+  dec.causal = causal;
+  dec.whole = whole_items(cache, batch) ? 1 : 0;
+  dec.scale_log2 = scale * 1.4426950408889634f;
+  fa::PrefillParams pre;
+  pre.b = dec.b;
+  pre.Q = dec.Q;
+  pre.ldq = ldq;
+  pre.O = dec.O;
+  pre.LSE = LSE;
+  pre.Ks = dec.Ks;
+  pre.Vs = dec.Vs;
+  pre.part_o = reinterpret_cast<float*>(wsb + ws.pre_o);
+  pre.part_ml = reinterpret_cast<float2*>(wsb + ws.pre_ml);
+  pre.G = G;
+  pre.Hq = Hq;
+  pre.min_rows = kDecodeMaxRows;
+  pre.causal = causal;
+  pre.scale_log2 = dec.scale_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (prm.rows == 8) return launch_decode_type<1>(cache->d, fp8, mk, mv, prm, n_cta, st);
-  return launch_decode_type<2>(cache->d, fp8, mk, mv, prm, n_cta, st);
+  return dec.rows == 8 ? launch_fwd_paged_type<1>(cache->d, fp8, m, dec, pre, many, st)
+                       : launch_fwd_paged_type<2>(cache->d, fp8, m, dec, pre, many, st);
 }
 
 }  // extern "C"

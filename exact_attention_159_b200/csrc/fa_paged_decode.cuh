@@ -43,6 +43,18 @@ constexpr int kDecStageBytes = 98304;
 constexpr int kDecMinTiles = 2;    // a CTA's share is at least this many tiles
 constexpr float kDecTau = 8.0f;    // log2 units
 constexpr float kScaleFloor = 7.8886090522101181e-31f;  // 2^-100: smaller value scales count as this
+constexpr float kBoost = 100.0f, kUnboost = kScaleFloor;
+
+// What the softmax needs of a page's scales: K's, log2 of V's, and, since w = 2^(s + log2 vs - m) of a page
+// of tiny values (a page of zeros has the smallest scale) would vanish beside others' while its keys still
+// count in the sum, a boost: w' = 2^(s + log2 vs + boost - m), w = w' 2^-boost, sum += w' (2^-boost / vs).
+// x: K scale, y: log2 of V's, z: 2^-boost / V scale, w: boost (0, or 100 for scales below 2^-40).
+__device__ __forceinline__ float4 page_scales(float ks, float vs) {
+  vs = fmaxf(vs, kScaleFloor);
+  const float lv = log2f(vs);
+  const bool tiny = lv < -40.0f;
+  return make_float4(ks, lv, (tiny ? kUnboost : 1.0f) / vs, tiny ? kBoost : 0.0f);
+}
 
 struct DecodeParams {
   PagedBatch b;
@@ -71,7 +83,7 @@ struct DecodeLayout {
   static constexpr int kV = kStages * kTileBytes;
   static constexpr int kMerge = 2 * kV;              // two warps' accumulators, eight query rows at a time
   static constexpr int kMergeWarp = (D / 16) * 512 + 512;  // a float4 per lane and column tile, then (m, l) x 2
-  static constexpr int kMeta = kMerge + 2 * kMergeWarp;    // [stage][box] (K scale, log2 V scale, 1 / V scale, -)
+  static constexpr int kMeta = kMerge + 2 * kMergeWarp;    // [stage][box] page_scales
   static constexpr int kBar = kMeta + kStages * kBoxes * 16;
   static constexpr int kMisc = kBar + 2 * kStages * 8;
   static constexpr int kBytes = kMisc + 96;
@@ -320,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc);
   long long* scratch = reinterpret_cast<long long*>(smem + L::kMisc + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependency_launch();
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) atomicCAS(prm.b.status, 0, kSiteDecode | 0x7F);
     return;
@@ -334,7 +346,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     fence_mbar_init();
   }
   const DecodeShare share = decode_share<kDecThreads>(prm, blockIdx.x, gridDim.x, scratch);  // has the barriers
-  if (share.b >= prm.b.B) return;
+  if (share.b >= prm.b.B) {
+    grid_dependency_wait();
+    return;
+  }
   const Guard g{abort_flag, prm.b.status};
   DecodeWalk w;
   w.start(prm, share, blockIdx.x);
@@ -366,8 +381,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           page = i < n_pages ? load_page(prm.b, w.b, i) : -1;
           if (FP8 && page >= 0) {
             const size_t at = static_cast<size_t>(page) * prm.b.Hkv + h;
-            const float vs = fmaxf(prm.Vs[at], kScaleFloor);
-            sc = make_float4(prm.Ks[at], log2f(vs), 1.0f / vs, 0.0f);
+            sc = page_scales(prm.Ks[at], prm.Vs[at]);
           }
         }
         const int my_page = __shfl_sync(0xffffffffu, page, (first_page + lane) & 31);
@@ -376,6 +390,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           my_sc.x = __shfl_sync(0xffffffffu, sc.x, (first_page + lane) & 31);
           my_sc.y = __shfl_sync(0xffffffffu, sc.y, (first_page + lane) & 31);
           my_sc.z = __shfl_sync(0xffffffffu, sc.z, (first_page + lane) & 31);
+          my_sc.w = __shfl_sync(0xffffffffu, sc.w, (first_page + lane) & 31);
         }
         const int st = it % S;
         if (!(ok = wait_warp(&empty[st], ((it / S) & 1) ^ 1, g, kSiteDecode | 1))) break;
@@ -403,6 +418,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         while (!mbar_try_wait(&full[i % S], (i / S) & 1) && globaltimer() - t0 < 200000000ull) {
         }
     }
+    // when another kernel of the call runs alongside, this one ends after it: what follows may rely on both
+    grid_dependency_wait();
     return;
   }
 
@@ -537,17 +554,19 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           }
         }
         // ---- softmax: scores in log2 units (plus log2 of the value scale)
-        float inv_vs[NS];
+        float inv_vs[NS], boost[NS];
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           float ks = 1.0f, lv = 0.0f;
           inv_vs[s] = 1.0f;
+          boost[s] = 0.0f;
           if constexpr (FP8) {
             if (s == 0 || key0 + 16 * s < len) {  // a page behind the end brought no scales
               const float4 sc = meta[st * L::kBoxes + ((row0 + 16 * s) >> box_shift)];
               ks = sc.x;
               lv = sc.y;
               inv_vs[s] = sc.z;
+              boost[s] = sc.w;
             }
           }
 #pragma unroll
@@ -612,10 +631,12 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           const float m1 = acc.m[n][1] == -INFINITY ? 0.0f : acc.m[n][1];
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            const float p0 = exp2_sfu(c[s][n][0] - m0), p1 = exp2_sfu(c[s][n][1] - m1);
-            const float p2 = exp2_sfu(c[s][n][2] - m0), p3 = exp2_sfu(c[s][n][3] - m1);
+            const float d0 = FP8 ? boost[s] - m0 : -m0, d1 = FP8 ? boost[s] - m1 : -m1;
+            float p0 = exp2_sfu(c[s][n][0] + d0), p1 = exp2_sfu(c[s][n][1] + d1);
+            float p2 = exp2_sfu(c[s][n][2] + d0), p3 = exp2_sfu(c[s][n][3] + d1);
             acc.l[n][0] = FP8 ? fmaf(p0 + p2, inv_vs[s], acc.l[n][0]) : acc.l[n][0] + (p0 + p2);
             acc.l[n][1] = FP8 ? fmaf(p1 + p3, inv_vs[s], acc.l[n][1]) : acc.l[n][1] + (p1 + p3);
+            if (FP8 && boost[s] > 0.0f) p0 *= kUnboost, p1 *= kUnboost, p2 *= kUnboost, p3 *= kUnboost;
             pf[s][n][0] = transpose8x8(FP8 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1));
             pf[s][n][1] = transpose8x8(FP8 ? pack_half2(p2, p3) : pack_bf16x2(p2, p3));
           }
@@ -744,50 +765,6 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       }
     }
   } while (w.next(prm));
-}
-
-// Joins the items that cuts divide: block c looks at the cut before CTA c's share, and joins the item it
-// falls into when no earlier cut does.  One thread per four columns of a row.
-constexpr int kJoinThreads = 128;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeParams prm, int n_cta) {
-  __shared__ long long scratch[kJoinThreads / 32 + 2];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the shares' sums are written
-  const int c = blockIdx.x + 1;
-  const DecodeShare s = decode_share<kJoinThreads>(prm, c, n_cta, scratch);
-  if (s.b >= prm.b.B) return;
-  const DecodeSeq d = decode_seq(prm, s.b);
-  const DecodeCut cut = decode_cut(s.per, c, s.off, d.tiles);
-  if (cut.last < c || cut.first != c - 1) return;
-  const int item = cut.item, last = cut.last;
-  const int h = item % prm.b.Hkv, rb = item / prm.b.Hkv;
-  const int rows = min(prm.rows, d.s.rows * prm.G - rb * prm.rows);
-  auto slot = [&](int cta) { return static_cast<size_t>(decode_slot(cta, cta - (c - 1))) * prm.rows; };
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
-    const int lr = i / (D / 4), col = (i % (D / 4)) * 4;
-    float m = -INFINITY;
-    for (int k = c - 1; k <= last; ++k) m = fmaxf(m, prm.part_ml[slot(k) + lr].x);
-    const float ms = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = c - 1; k <= last; ++k) {
-      const float2 ml = prm.part_ml[slot(k) + lr];
-      const float4 v = *reinterpret_cast<const float4*>(prm.part_o + (slot(k) + lr) * D + col);
-      const float f = exp2f(ml.x - ms);
-      l = fmaf(f, ml.y, l);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int row = rb * prm.rows + lr;
-    const size_t at = static_cast<size_t>(d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G;
-    *reinterpret_cast<uint2*>(prm.O + at * D + col) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (col == 0) prm.LSE[at] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-  }
 }
 
 }  // namespace fa

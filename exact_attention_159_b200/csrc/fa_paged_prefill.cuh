@@ -1,0 +1,751 @@
+// fa_paged_prefill.cuh -- attention of many query rows (prompt chunks, verified drafts of wide groups) over
+// the paged cache on the 5th-generation tensor cores.
+//
+// The pipeline is that of the contiguous forward (fa_fwd.cuh): two 128-row query tiles in flight per CTA,
+// S = Q K^T into TMEM, one thread per score row for the online softmax with conditional rescaling, P back
+// over S in TMEM, O += P V.  What the cache changes:
+//   Rows.  The R = rows * G (token, query head) pairs that read one key/value head are the rows, so a key
+//     tile is read once for all G heads; 256 of them are a pair of tiles.
+//   Work.  A CTA per SM walks an equal share of all (sequence, key/value head, pair) items' key tiles laid
+//     end to end, so neither a batch of ragged prompts nor a single chunk of few pairs leaves SMs idle; an
+//     item that a cut divides leaves unnormalised fp32 sums for the join.  The number of tiles that a pair
+//     sees under the causal mask is a floor of a linear function, whose sums have a closed form, so every
+//     CTA finds its share by itself.
+//   Pages.  A 128-key tile is one TMA box for each of its pages.  Slots behind the sequence's end may hold
+//     anything: their scores are masked, and their values are zeroed in shared memory before the MMA (a
+//     weight of zero times a NaN is not zero).
+//   e4m3.  Codes land in a staging tile; two warps turn them into halves (exact) in the operand tiles, at about
+//     a quarter of the time that an iteration leaves them.  The scales stay outside the products: K's
+//     multiplies the scores of its 16 columns or more, V's joins the exponent (w = 2^(s + log2 vs - m),
+//     O = sum w * code, the softmax's sum is sum w / vs).  Q becomes halves by a power of two per row, P is
+//     rounded to half.
+#pragma once
+
+#include "exp2_poly.cuh"
+#include "fa_fwd.cuh"
+#include "fa_paged.cuh"
+#include "fa_paged_decode.cuh"
+
+namespace fa {
+
+constexpr int kSitePrefill = 0xC00;
+constexpr int kPreCtas = 148;
+constexpr int kPreRows = 256;     // query rows of an item: two tiles
+constexpr int kPreMinTiles = 2;   // a CTA's share is at least this many key tiles
+
+struct PrefillParams {
+  PagedBatch b;
+  const __nv_bfloat16* Q;  // [T, Hq, D], ldq elements between tokens
+  long long ldq;
+  __nv_bfloat16* O;   // [T, Hq, D]
+  float* LSE;         // [T, Hq]
+  const float *Ks, *Vs;
+  float* part_o;      // [2 * kPreCtas][kPreRows][D] unnormalised sums
+  float2* part_ml;    // [2 * kPreCtas][kPreRows] (m in log2 units, l)
+  int G, Hq;
+  int min_rows;       // sequences of no more rows * G are the other kernel's
+  int causal;
+  float scale_log2;
+};
+
+template <int D, bool FP8>
+struct PrefillLayout {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kRawBytes = FP8 ? kTile * D : 0;  // e4m3 staging of one tile
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTileBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kRawK = kV + kStages * kTileBytes;
+  static constexpr int kRawV = kRawK + kRawBytes;
+  static constexpr int kMeta = kRawV + kRawBytes;  // [8 tiles][8 groups of 16 keys] page_scales
+  static constexpr int kBar = kMeta + (FP8 ? 8 * 8 * 16 : 0);
+  // q_full[2], k_full[S], v_full[S], k_empty[S], v_empty[S], v_land[S], s_full[2], p_full[2], o_full[2], drain,
+  // kraw_full, kraw_empty, vraw_full, vraw_empty
+  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 4;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 16 + 16 * 8;
+  static constexpr int kThreads = 384;
+  static constexpr int kLaunchRegs = (65536 / kThreads) / 8 * 8;
+  static_assert(kBytes <= 232448, "more shared memory than a CTA may have");
+};
+
+// Halves: the instruction descriptor of bf16 without its two type bits.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// ------------------------------------------------------------------------------------- the plan
+// Sum of floor((a i + b) / m) over i = 0 .. n - 1 (all non-negative, m > 0): Euclid's steps on the lattice points
+// under the line.
+FA_HD long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long x = m;
+    m = a;
+    a = x;
+  }
+  return sum;
+}
+
+struct PrefillSeq {
+  SeqInfo s;
+  int pairs;       // 0: no rows, or too few for this kernel
+  int tiles;       // key tiles of the whole sequence (1 when it has no key: its rows are written)
+  int linear;      // pair p counts (x + 2 p) / G + 1 tiles, the last one all; otherwise every pair counts all
+  long long x;
+  int G;
+  // Tiles counted before pair p (p < pairs), and pair p's own; a pair's rows see no tile beyond its own.
+  FA_HD long long before(int p) const {
+    return linear ? p + floor_sum(p, G, 2, x) : static_cast<long long>(p) * tiles;
+  }
+  FA_HD int count(int p) const {
+    return linear && p < pairs - 1 ? static_cast<int>((x + 2 * p) / G) + 1 : tiles;
+  }
+  FA_HD long long head_units() const { return pairs == 0 ? 0 : before(pairs - 1) + tiles; }
+};
+FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
+  PrefillSeq d;
+  d.s = load_seq(p.b, b);
+  d.G = p.G;
+  const long long rows = static_cast<long long>(d.s.rows) * p.G;
+  d.pairs = rows > p.min_rows ? static_cast<int>((rows + kPreRows - 1) / kPreRows) : 0;
+  d.tiles = max(1, (d.s.len + 127) / 128);
+  // pair p's last row (when the pair is full) is token (256 (p + 1) - 1) / G, which sees keys up to len - rows +
+  // that; a tile has 128 keys, and 256 p is a multiple of 128, which leaves (x + 2 p) / G
+  d.linear = p.causal && d.s.len >= d.s.rows;
+  d.x = d.linear ? (static_cast<long long>(d.s.len - d.s.rows) * p.G + 255) / 128 : 0;
+  return d;
+}
+FA_HD long long prefill_per(long long total) {
+  const long long per = (total + kPreCtas - 1) / kPreCtas;
+  return per < kPreMinTiles ? kPreMinTiles : per;
+}
+// Unit `off` of a sequence: head, pair and tile.
+struct PrefillAt {
+  int h, p, tile;
+};
+FA_HD PrefillAt prefill_at(const PrefillSeq& d, long long off) {
+  PrefillAt a;
+  const long long head = d.head_units();
+  a.h = static_cast<int>(off / head);
+  const long long r = off % head;
+  int lo = 0, hi = d.pairs - 1;  // the last pair that begins at r or before
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (d.before(mid) <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  a.p = lo;
+  a.tile = static_cast<int>(r - d.before(lo));
+  return a;
+}
+
+// The item that the cut before share c falls into: `first`..`last` are the shares it lies in (as DecodeCut).
+struct PrefillCut {
+  int first, last;
+};
+FA_HD PrefillCut prefill_cut(long long per, int c, const PrefillAt& a, int n) {
+  const long long begin = per * c - a.tile;
+  PrefillCut r;
+  r.first = static_cast<int>(begin / per);
+  r.last = a.tile == 0 ? c - 1 : static_cast<int>((begin + n - 1) / per);
+  return r;
+}
+
+struct PrefillShare {
+  long long total, per, off;
+  int b;
+};
+// As decode_share, over the units of this kernel.
+template <int THREADS>
+__device__ __forceinline__ PrefillShare prefill_share(const PrefillParams& p, int index, long long* scratch) {
+  constexpr int W = THREADS / 32;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int run = (p.b.B + THREADS - 1) / THREADS;
+  const int b0 = min(t * run, p.b.B), b1 = min(b0 + run, p.b.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += prefill_seq(p, b).head_units() * p.b.Hkv;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  if (t == 0) scratch[W] = p.b.B, scratch[W + 1] = 0;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  PrefillShare r;
+  r.total = total;
+  r.per = prefill_per(total);
+  const long long want = r.per * index;
+  const long long lo = before + inc - mine;
+  if (want >= lo && want < lo + mine) {
+    long long at = lo;
+    for (int b = b0; b < b1; ++b) {
+      const long long u = prefill_seq(p, b).head_units() * p.b.Hkv;
+      if (want < at + u) {
+        scratch[W] = b;
+        scratch[W + 1] = want - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  r.b = static_cast<int>(scratch[W]);
+  r.off = scratch[W + 1];
+  return r;
+}
+
+// Walks a CTA's share: one segment (key tiles [t0, t1) of an item) after another.
+struct PrefillWalk {
+  long long left;
+  int b, h, p, t0, t1, n;  // n: the item's tiles
+  bool whole;
+  PrefillSeq d;
+  FA_HD void start(const PrefillParams& prm, const PrefillShare& s, int index) {
+    left = min(s.per, s.total - s.per * index);
+    b = s.b;
+    d = prefill_seq(prm, b);
+    const PrefillAt a = prefill_at(d, s.off);
+    h = a.h;
+    p = a.p;
+    t0 = a.tile;
+    cut();
+  }
+  FA_HD void cut() {
+    n = d.count(p);
+    t1 = static_cast<int>(min(static_cast<long long>(n), t0 + left));
+    whole = t0 == 0 && t1 == n;
+  }
+  FA_HD bool next(const PrefillParams& prm) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++p == d.pairs) {
+      p = 0;
+      if (++h == prm.b.Hkv) {
+        h = 0;
+        do {
+          if (++b >= prm.b.B) return false;
+          d = prefill_seq(prm, b);
+        } while (d.pairs == 0);
+      }
+    }
+    cut();
+    return true;
+  }
+  // The first key tile that query tile t does not see within this segment (t0: it sees none of it).
+  FA_HD int end(const PrefillParams& prm, int t) const {
+    const int rows = d.s.rows * prm.G, row0 = p * kPreRows + t * kTile;
+    if (row0 >= rows) return t0;
+    const int last_row = min(row0 + kTile, rows) - 1;
+    const int last = prm.causal ? d.s.len - d.s.rows + last_row / prm.G : d.s.len - 1;
+    const int seen = last < 0 ? 0 : min(last / kTile + 1, (d.s.len + kTile - 1) / kTile);
+    return max(t0, min(t1, seen));
+  }
+};
+
+// --------------------------------------------------------------------------------------- kernel
+template <int D, bool FP8>
+__global__ void __launch_bounds__(384, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const PrefillParams prm) {
+  using L = PrefillLayout<D, FP8>;
+  constexpr int S = L::kStages;
+  constexpr int T = L::kTileBytes;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  grid_dependency_launch();
+  if ((smem_u32(smem) & 1023u) != 0) {  // swizzled tiles need a 1024-byte aligned base
+    if (threadIdx.x == 0) atomicCAS(prm.b.status, 0, kSitePrefill | 0x7F);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 2;
+  uint64_t* v_full = k_full + S;
+  uint64_t* k_empty = v_full + S;
+  uint64_t* v_empty = k_empty + S;
+  uint64_t* v_land = v_empty + S;  // bf16: V's copies have landed (v_full: and what is behind the end is zero)
+  uint64_t* s_full = v_land + S;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* drain = o_full + 2;
+  uint64_t* kraw_full = drain + 1;
+  uint64_t* kraw_empty = kraw_full + 1;
+  uint64_t* vraw_full = kraw_empty + 1;
+  uint64_t* vraw_empty = vraw_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
+  long long* scratch = reinterpret_cast<long long*>(smem + L::kMisc + 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const PrefillShare share = prefill_share<384>(prm, blockIdx.x, scratch);
+  if (share.b >= prm.b.B) return;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_land[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 128);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&o_full[t], 1);
+    }
+    for (uint64_t* b : {drain, kraw_full, kraw_empty, vraw_full, vraw_empty}) mbar_init(b, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Guard g{abort_flag, prm.b.status};
+  PrefillWalk w;
+  w.start(prm, share, blockIdx.x);
+
+  if (warp < 4) {
+    regs_to<kFwdRegsCtl, L::kLaunchRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------------------- producer
+      // Lane i issues the boxes of a tile's i-th page.
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+      const int shift = min(prm.b.page_shift, 7), box_rows = 1 << shift;
+      constexpr int kCols = FP8 ? D : 64;
+      bool ok = true;
+      int kt = 0, k_issued = 0, v_issued = 0;  // key tiles since the start
+      do {
+        const int end = max(w.end(prm, 0), w.end(prm, 1));
+        for (int j = w.t0; j < end && ok; ++j, ++kt) {
+          const int keys = min(kTile, w.d.s.len - j * kTile);
+          const int boxes = (keys + box_rows - 1) >> shift;
+          const int first_page = (j * kTile) >> prm.b.page_shift;
+          int z = 0;
+          float4 sc = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+          if (lane < boxes) {
+            const int page = load_page(prm.b, w.b, first_page + lane);
+            // a page out of range reads as zeros beyond the map's last head
+            z = page >= 0 ? page * prm.b.Hkv + w.h : prm.b.num_pages * prm.b.Hkv;
+            if (FP8 && page >= 0)
+              sc = page_scales(prm.Ks[z], prm.Vs[z]);
+          }
+          const int s = kt % S;
+          const uint32_t ph = (kt / S) & 1;
+          uint64_t* full = FP8 ? kraw_full : &k_full[s];
+          ok = wait_warp(FP8 ? kraw_empty : &k_empty[s], FP8 ? (kt & 1) ^ 1 : ph ^ 1, g, kSitePrefill | 1);
+          if (!ok) break;
+          if (FP8 && lane < boxes) {
+            // the scales of the page's groups of 16 keys; of the eight slots the one written here was last
+            // read for tile kt - 8, and the S that the operand ring has already seen done come after that
+            float4* m = reinterpret_cast<float4*>(smem + L::kMeta) + (kt & 7) * 8 + (lane << (shift - 4));
+            for (int i = 0; i < 1 << (shift - 4); ++i) m[i] = sc;
+          }
+          __syncwarp();
+          const int bytes = boxes * box_rows * D * (FP8 ? 1 : 2);
+          if (lane == 0) mbar_expect_tx(full, bytes);
+          __syncwarp();
+          uint8_t* to = smem + (FP8 ? L::kRawK : L::kK + s * T) + lane * box_rows * kCols * (FP8 ? 1 : 2);
+          if (lane < boxes)
+            for (int c = 0; c < D / kCols; ++c) tma_load_3d(to + c * 16384, &tmK, c * kCols, 0, z, full);
+          ++k_issued;
+          full = FP8 ? vraw_full : &v_land[s];
+          if (!(ok = wait_warp(FP8 ? vraw_empty : &v_empty[s], FP8 ? (kt & 1) ^ 1 : ph ^ 1, g, kSitePrefill | 2))) break;
+          if (lane == 0) mbar_expect_tx(full, bytes);
+          __syncwarp();
+          to = smem + (FP8 ? L::kRawV : L::kV + s * T) + lane * box_rows * kCols * (FP8 ? 1 : 2);
+          if (lane < boxes)
+            for (int c = 0; c < D / kCols; ++c) tma_load_3d(to + c * 16384, &tmV, c * kCols, 0, z, full);
+          ++v_issued;
+        }
+      } while (ok && w.next(prm));
+      if (!ok) {  // let copies already in flight land before the CTA exits
+        constexpr int R = FP8 ? 1 : S;
+        for (int i = max(k_issued - R, 0); i < k_issued; ++i) drain_wait(FP8 ? kraw_full : &k_full[i % R], (i / R) & 1);
+        for (int i = max(v_issued - R, 0); i < v_issued; ++i) drain_wait(FP8 ? vraw_full : &v_land[i % R], (i / R) & 1);
+      }
+    } else if (warp == 1) {
+      // --------------------------------------------------------------------------------- MMA
+      // One thread issues every UMMA, in the order of the contiguous forward.
+      if (lane == 0) {
+        constexpr uint32_t idS = FP8 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t idO = FP8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
+        const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
+        auto issue_s = [&](int t, int s) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            mma_ss(tmem + 128 * t, sdesc_sw128(sQ + t * T + off, 16, 1024), sdesc_sw128(sK + s * T + off, 16, 1024),
+                   idS, kk > 0);
+          }
+        };
+        auto issue_pv = [&](int t, int s, bool acc) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, sdesc_sw128(sV + s * T + kk * 2048, 16384, 1024), idO,
+                   (acc || kk > 0) ? 1u : 0u);
+        };
+        bool ok = true;
+        int kt = 0;
+        int qn[2] = {0, 0}, steps[2] = {0, 0};  // query tiles loaded, tile steps done
+        do {
+          const int end[2] = {w.end(prm, 0), w.end(prm, 1)};
+          const int last = max(end[0], end[1]);
+          if (last == w.t0) continue;
+          if (!(ok = wait(&k_full[kt % S], (kt / S) & 1, g, kSitePrefill | 3))) break;
+          for (int t = 0; t < 2 && ok; ++t)
+            if (end[t] > w.t0) {
+              if (!(ok = wait(&q_full[t], qn[t]++ & 1, g, kSitePrefill | 4))) break;
+              tc_fence_after();
+              issue_s(t, kt % S);
+              tc_commit(&s_full[t]);
+            }
+          if (!ok) break;
+          tc_commit(&k_empty[kt % S]);
+          for (int j = w.t0; ok && j < last; ++j, ++kt) {
+            const int s = kt % S, s1 = (kt + 1) % S;
+            if (!(ok = wait(&v_full[s], (kt / S) & 1, g, kSitePrefill | 5))) break;
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (j >= end[t]) continue;
+              if (!(ok = wait(&p_full[t], steps[t]++ & 1, g, kSitePrefill | 7))) break;
+              tc_fence_after();
+              issue_pv(t, s, j > w.t0);
+              tc_commit(&o_full[t]);
+              if (j + 1 < end[t]) {
+                if (!(ok = wait(&k_full[s1], ((kt + 1) / S) & 1, g, kSitePrefill | 8))) break;
+                tc_fence_after();
+                issue_s(t, s1);
+                tc_commit(&s_full[t]);
+              }
+            }
+            if (ok) {
+              tc_commit(&v_empty[s]);
+              if (j + 1 < last) tc_commit(&k_empty[s1]);
+            }
+          }
+        } while (ok && w.next(prm));
+        tc_commit(drain);
+        drain_wait(drain, 0);
+      }
+    } else if constexpr (FP8) {
+      // ----------------------------------------------- e4m3 to halves: warp 2 K, warp 3 V
+      const bool is_v = warp == 3;
+      uint64_t *rfull = is_v ? vraw_full : kraw_full, *rempty = is_v ? vraw_empty : kraw_empty;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+      const uint32_t raw = smem_u32(smem + (is_v ? L::kRawV : L::kRawK));
+      bool ok = true;
+      int kt = 0;
+      do {
+        const int end = max(w.end(prm, 0), w.end(prm, 1));
+        for (int j = w.t0; j < end && ok; ++j, ++kt) {
+          const int s = kt % S;
+          if (!(ok = wait_warp(rfull, kt & 1, g, kSitePrefill | 9))) break;
+          if (!(ok = wait_warp(&empty[s], ((kt / S) & 1) ^ 1, g, kSitePrefill | 10))) break;
+          const int live = w.d.s.len - j * kTile;  // rows behind it become zeros
+          const uint32_t to = smem_u32(smem + (is_v ? L::kV : L::kK) + s * T);
+          constexpr int CH = D / 16;  // 16-byte chunks of a row of codes
+          // eight lanes store rows r and r + 1 (of 4 chunks each): no two to the same bank
+#pragma unroll 4
+          for (int i = 0; i < kTile * CH / 32; ++i) {
+            int r, c;
+            if constexpr (D == 128) {
+              r = (i >> 1) * 8 + (lane >> 2), c = (lane & 3) + 4 * (i & 1);
+            } else {
+              r = i * 8 + (lane >> 2), c = lane & 3;
+            }
+            const uint32_t from = D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4) : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+            uint4 x = lds128(from);
+            if (r >= live) x = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t h[8];
+            halves_of_e4m3(x.x, h[0], h[1]);
+            halves_of_e4m3(x.y, h[2], h[3]);
+            halves_of_e4m3(x.z, h[4], h[5]);
+            halves_of_e4m3(x.w, h[6], h[7]);
+            const uint32_t at = to + (c >> 2) * 16384 + r * 128, c2 = 2 * (c & 3);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2) ^ (r & 7)) << 4)), "r"(h[0]),
+                         "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2 + 1) ^ (r & 7)) << 4)), "r"(h[4]),
+                         "r"(h[5]), "r"(h[6]), "r"(h[7])
+                         : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[s]);
+            mbar_arrive(rempty);
+          }
+        }
+      } while (ok && w.next(prm));
+    } else if (warp == 3) {
+      // ------------------------------------------- values behind a sequence's end become zeros
+      bool ok = true;
+      int kt = 0;
+      do {
+        const int end = max(w.end(prm, 0), w.end(prm, 1));
+        for (int j = w.t0; j < end && ok; ++j, ++kt) {
+          const int live = w.d.s.len - j * kTile, s = kt % S;
+          if (!(ok = wait_warp(&v_land[s], (kt / S) & 1, g, kSitePrefill | 11))) break;
+          if (live < kTile) {
+            for (int i = lane; i < (kTile - live) * 8; i += 32)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<uint4*>(smem + L::kV + s * T + c * 16384 + live * 128 + i * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&v_full[s]);
+        }
+      } while (ok && w.next(prm));
+    }
+  } else {
+    regs_to<kFwdRegsSoftmax, L::kLaunchRegs>();
+    // ------------------------------------------- Q, softmax / correction / epilogue: a thread a row
+    const int t = (warp - 4) >> 2;   // query tile
+    const int quarter = warp & 3;    // TMEM lanes this warp may touch
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + 128 * t + lane_off;
+    const uint32_t tO = tmem + 256 + D * t + lane_off;
+    const float4* meta = reinterpret_cast<const float4*>(smem + L::kMeta);
+    bool ok = true;
+    int step = 0, kt0 = 0;  // this tile's steps, key tiles of the CTA before the segment
+    do {
+      const int ends[2] = {w.end(prm, 0), w.end(prm, 1)};
+      const int end = ends[t];
+      const int row = w.p * kPreRows + t * kTile + r;  // of the sequence's rows * G
+      const bool real = row < w.d.s.rows * prm.G;
+      const int token = real ? row / prm.G : 0, head = w.h * prm.G + (real ? row % prm.G : 0);
+      const int off = w.d.s.len - w.d.s.rows;
+      const int lim = prm.causal && real ? off + token : w.d.s.len - 1;  // last visible key
+      const int lim_min = prm.causal ? off + (w.p * kPreRows + t * kTile) / prm.G : w.d.s.len - 1;
+      float sl2 = prm.scale_log2;
+      if (end > w.t0) {
+        // this thread's row of Q; the tile's last S is done, since this thread has seen its scores
+        const uint4* q = reinterpret_cast<const uint4*>(prm.Q + static_cast<size_t>(w.d.s.row0 + token) * prm.ldq + head * D);
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = real ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (FP8) {
+          float amax = 0.0f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
+          }
+          // a power of two above the row's largest magnitude (kept where its inverse is normal)
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 2), 252);
+          sl2 *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = pack_half2(__uint_as_float(v[k] << 16) * down, __uint_as_float(v[k] & 0xFFFF0000u) * down);
+            x[i] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint4*>(smem + L::kQ + t * T + (i >> 3) * 16384 + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = x[i];
+        fence_proxy_async();
+        mbar_arrive(&q_full[t]);
+      }
+      float m_ref = -INFINITY, l = 0.0f;
+      for (int j = w.t0; j < end; ++j, ++step) {
+        if (!(ok = wait_warp(&s_full[t], step & 1, g, kSitePrefill | 12))) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence(sr[c]);
+#define S(c) __uint_as_float(sr[(c) >> 5][(c) & 31])
+        if (j * kTile + kTile - 1 > lim_min) {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (j * kTile + c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+        }
+        const float4* mt = meta + ((kt0 + j - w.t0) & 7) * 8;
+        // row maximum (e4m3: of each group of 16 keys, then with the group's scales)
+        float top;
+        if constexpr (FP8) {
+          float mg[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float m0 = fmax3(S(16 * q), S(16 * q + 1), S(16 * q + 2)), m1 = fmax3(S(16 * q + 3), S(16 * q + 4), S(16 * q + 5));
+            m0 = fmax3(m0, S(16 * q + 6), S(16 * q + 7));
+            m1 = fmax3(m1, S(16 * q + 8), S(16 * q + 9));
+            m0 = fmax3(m0, S(16 * q + 10), S(16 * q + 11));
+            m1 = fmax3(m1, S(16 * q + 12), S(16 * q + 13));
+            m0 = fmax3(m0, S(16 * q + 14), S(16 * q + 15));
+            const bool live = j * kTile + 16 * q < w.d.s.len;  // a page behind the end brought no scales
+            const float4 sc = mt[q];
+            // a group that is wholly masked stays at -inf whatever its scale (zero too)
+            const float x = fmaxf(m0, m1);
+            mg[q] = live && x > -INFINITY ? fmaf(x, sl2 * sc.x, sc.y) : -INFINITY;
+          }
+          top = fmaxf(fmax3(mg[0], mg[1], mg[2]), fmax3(mg[3], mg[4], fmax3(mg[5], mg[6], mg[7])));
+        } else {
+          float mx[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            mx[q] = S(32 * q);
+#pragma unroll
+            for (int c = 32 * q + 1; c < 32 * q + 31; c += 2) mx[q] = fmax3(mx[q], S(c), S(c + 1));
+            mx[q] = fmaxf(mx[q], S(32 * q + 31));
+          }
+          top = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sl2;
+        }
+        const float m_new = fmaxf(m_ref, top);
+        const bool need = m_new > m_ref + kRescaleTau;
+        const float alpha = need ? exp2_sfu(m_ref - m_new) : 1.0f;
+        if (need) {
+          l *= alpha;
+          m_ref = m_new;
+        }
+        const float m_sub = m_ref == -INFINITY ? 0.0f : m_ref;
+        float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
+        // P, 32 keys -> 16 columns at a time, over S
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float2 c2 = make_float2(sl2, sl2), nm2 = make_float2(-m_sub, -m_sub);
+            float inv = 1.0f;
+            bool tiny = false;
+            if constexpr (FP8) {
+              const bool live = j * kTile + 32 * cc + 16 * hh < w.d.s.len;
+              const float4 sc = mt[2 * cc + hh];
+              const float f = live ? fmaxf(sl2 * sc.x, 1e-37f) : 1.0f, n = live ? sc.y + sc.w - m_sub : 0.0f;
+              inv = live ? sc.z : 0.0f;
+              tiny = live && sc.w > 0.0f;
+              c2 = make_float2(f, f);
+              nm2 = make_float2(n, n);
+            }
+            float2 gs = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = 32 * cc + 16 * hh + 2 * e;
+              const float2 x = __ffma2_rn(make_float2(S(c), S(c + 1)), c2, nm2);
+              float2 p;
+              p.x = exp2_sfu(x.x);
+              p.y = exp2_sfu(x.y);
+              if constexpr (FP8) {
+                gs = __fadd2_rn(gs, p);
+                if (tiny) p.x *= kUnboost, p.y *= kUnboost;
+                pk[8 * hh + e] = pack_half2(p.x, p.y);
+              } else {
+                if (e & 1) ls1 = __fadd2_rn(ls1, p);
+                else ls0 = __fadd2_rn(ls0, p);
+                pk[8 * hh + e] = pack_bf16x2(p.x, p.y);
+              }
+            }
+            if constexpr (FP8) ls0 = __ffma2_rn(gs, make_float2(inv, inv), ls0);
+          }
+          tmem_st16(tS + 16 * cc, pk);
+        }
+#undef S
+        const float2 ls = __fadd2_rn(ls0, ls1);
+        l += ls.x + ls.y;
+        if (j > w.t0 && __any_sync(0xffffffffu, need)) {
+          // O_t *= alpha once the previous P.V has landed (before p_full lets the next one add to it)
+          ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 13);
+          tc_fence_after();
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * c, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + 32 * c, o);
+            }
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        if (!ok) break;
+        mbar_arrive(&p_full[t]);
+      }
+      if (!ok) break;
+      const size_t at = static_cast<size_t>(w.d.s.row0 + token) * prm.Hq + head;
+      const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, w.t0)) * kPreRows + t * kTile + r;
+      if (end > w.t0) {
+        if (!(ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 14))) break;
+        tc_fence_after();
+        const float scale = !w.whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+          reg_fence(o);
+          if (real && w.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(prm.O + at * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * scale, __uint_as_float(o[8 * i + 2 * k + 1]) * scale);
+              dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          } else if (real) {
+            uint4* dst = reinterpret_cast<uint4*>(prm.part_o + slot * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        tc_fence_before();
+      } else if (real && w.whole) {  // no key is visible to any row of the tile
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(prm.O + at * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (real) {
+        if (w.whole) prm.LSE[at] = l > 0.0f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        else prm.part_ml[slot] = make_float2(m_ref, l);  // m = -inf: the join takes nothing from this part
+      }
+      kt0 += max(ends[0], ends[1]) - w.t0;
+    } while (w.next(prm));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fa

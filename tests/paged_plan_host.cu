@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "fa_paged_decode.cuh"
+#include "fa_paged_prefill.cuh"
 
 #define REQUIRE(x)                                                      \
   do {                                                                  \
@@ -136,10 +137,129 @@ static void shares(std::mt19937& rng, bool whole) {
   REQUIRE(status == 0);
 }
 
+static void many_rows(std::mt19937& rng) {
+  auto pick = [&](int lo, int hi) { return lo + static_cast<int>(rng() % static_cast<unsigned>(hi - lo + 1)); };
+  const int B = pick(1, 6);
+  std::vector<int> cu{0}, lens;
+  for (int b = 0; b < B; ++b) {
+    const int q = pick(0, 3) == 0 ? pick(0, 3) : pick(0, 900);
+    cu.push_back(cu.back() + q);
+    lens.push_back(pick(0, 4) == 0 ? pick(0, 900) : q + pick(0, 3000));
+  }
+  int status = 0;
+  PrefillParams p{};
+  p.b.cu_q = cu.data();
+  p.b.lens = lens.data();
+  p.b.B = B;
+  p.b.T = cu.back();
+  p.b.max_q = 900;
+  p.b.max_pages = 1000;
+  p.b.page_shift = 4;
+  p.b.num_pages = 1;
+  p.b.Hkv = pick(1, 4);
+  p.b.status = &status;
+  p.G = pick(1, 9);
+  p.min_rows = pick(0, 1) ? 32 : 200;
+  p.causal = pick(0, 3) != 0;
+  long long total = 0;
+  std::vector<long long> units;
+  for (int b = 0; b < B; ++b) {
+    const PrefillSeq d = prefill_seq(p, b);
+    REQUIRE((d.pairs == 0) == (static_cast<long long>(d.s.rows) * p.G <= p.min_rows));
+    long long sum = 0;
+    for (int k = 0; k < d.pairs; ++k) {
+      REQUIRE(d.before(k) == sum);
+      sum += d.count(k);
+      // a pair's rows see none but its own tiles
+      const int last_row = std::min((k + 1) * kPreRows, d.s.rows * p.G) - 1;
+      const int last = p.causal ? d.s.len - d.s.rows + last_row / p.G : d.s.len - 1;
+      const int seen = last < 0 ? 0 : std::min(last, d.s.len - 1) / 128 + 1;
+      REQUIRE(d.count(k) >= std::max(seen, 1));
+      if (d.linear && seen > 0) REQUIRE(d.count(k) == seen);
+    }
+    REQUIRE(d.head_units() == sum);
+    units.push_back(sum * p.b.Hkv);
+    total += units.back();
+  }
+  const long long per = prefill_per(total);
+  REQUIRE(per * kPreCtas >= total);
+  auto locate = [&](int c) {
+    PrefillShare s{total, per, 0, B};
+    long long at = 0;
+    for (int b = 0; b < B; ++b) {
+      if (per * c >= at && per * c < at + units[b]) s.b = b, s.off = per * c - at;
+      at += units[b];
+    }
+    return s;
+  };
+  using Item = std::vector<int>;
+  std::map<Item, std::vector<int>> seen, parts;
+  std::map<int, int> slots;
+  for (int c = 0; c < kPreCtas; ++c) {
+    const PrefillShare s = locate(c);
+    if (s.b >= B) continue;
+    PrefillWalk w;
+    w.start(p, s, c);
+    do {
+      REQUIRE(w.p >= 0 && w.p < w.d.pairs && w.h < p.b.Hkv && w.t0 >= 0 && w.t0 < w.t1 && w.t1 <= w.n);
+      for (int t = 0; t < 2; ++t) {
+        const int end = w.end(p, t), first = w.p * kPreRows + t * kTile;
+        REQUIRE(end >= w.t0 && end <= w.t1 && end * 128 < w.d.s.len + 128);
+        if (first >= w.d.s.rows * p.G) REQUIRE(end == w.t0);
+        // every visible key of every row of the tile is in a tile below `end`, or in another segment
+        for (int r = first; r < std::min(first + kTile, w.d.s.rows * p.G); ++r) {
+          const int last = std::min(w.d.s.len - 1, p.causal ? w.d.s.len - w.d.s.rows + r / p.G : w.d.s.len - 1);
+          if (last >= w.t0 * 128) REQUIRE(end >= std::min(w.t1, last / 128 + 1));
+        }
+      }
+      auto& v = seen[{w.b, w.h, w.p}];
+      v.resize(w.n);
+      for (int t = w.t0; t < w.t1; ++t) ++v[t];
+      if (!w.whole) {
+        const int slot = decode_slot(c, w.t0);
+        REQUIRE(slot >= 0 && slot < 2 * kPreCtas && slots[slot]++ == 0);
+        parts[{w.b, w.h, w.p}].push_back(slot);
+      }
+    } while (w.next(p));
+  }
+  long long items = 0;
+  for (int b = 0; b < B; ++b) items += static_cast<long long>(prefill_seq(p, b).pairs) * p.b.Hkv;
+  REQUIRE(static_cast<long long>(seen.size()) == items);
+  for (auto& kv : seen)
+    for (int n : kv.second) REQUIRE(n == 1);
+  for (int c = 1; c < kPreCtas; ++c) {
+    const PrefillShare s = locate(c);
+    if (s.b >= B) continue;
+    const PrefillSeq d = prefill_seq(p, s.b);
+    const PrefillAt a = prefill_at(d, s.off);
+    const PrefillCut cut = prefill_cut(per, c, a, d.count(a.p));
+    if (cut.last < c || cut.first != c - 1) continue;
+    auto it = parts.find({s.b, a.h, a.p});
+    REQUIRE(it != parts.end());
+    std::vector<int> want;
+    for (int k = c - 1; k <= cut.last; ++k) want.push_back(decode_slot(k, k - (c - 1)));
+    REQUIRE(it->second == want);
+    parts.erase(it);
+  }
+  REQUIRE(parts.empty());
+}
+
+static void sums() {
+  for (long long m = 1; m < 12; ++m)
+    for (long long a = 0; a < 9; ++a)
+      for (long long b = 0; b < 60; b += 7)
+        for (long long n = 0, s = 0; n < 40; ++n) {
+          REQUIRE(floor_sum(n, m, a, b) == s);
+          s += (a * n + b) / m;
+        }
+}
+
 int main() {
+  sums();
   bad_indices();
   std::mt19937 rng(1);
   for (int i = 0; i < 20000; ++i) shares(rng, i % 4 == 0);
+  for (int i = 0; i < 3000; ++i) many_rows(rng);
   std::printf("ok\n");
   return 0;
 }
