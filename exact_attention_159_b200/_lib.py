@@ -86,6 +86,8 @@ def lib_path() -> str:
 def lib():
     """Load libfa.so once; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = lib_path()

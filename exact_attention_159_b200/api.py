@@ -6,7 +6,6 @@ computation runs in the library's kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -20,13 +19,13 @@ _E4M3 = torch.float8_e4m3fn
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _shape(q: torch.Tensor):
@@ -286,34 +285,47 @@ class PagedBatch:
         self._ref = ctypes.byref(self._c)
 
 
-def _need_rows(t: torch.Tensor, name: str, heads: int, d: int, rows: int | None = None) -> int:
-    """Checks token-major rows [T, heads, d] with each row contiguous; returns the elements between rows."""
-    if t.dtype != _BF16 or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (
-            rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: expected CUDA {_BF16} [{'T' if rows is None else rows}, {heads}, {d}], got "
-                         f"{t.dtype} {tuple(t.shape)} cuda={t.is_cuda}")
-    if t.shape[0] == 0 or heads == 0:
-        return heads * d
+def _need_rows(t: torch.Tensor, name: str, heads: int, d: int, rows: int, device: int) -> int:
+    """Checks token-major rows [rows, heads, d] with each row contiguous; returns the elements between rows."""
+    if t.dtype != _BF16 or not t.is_cuda or tuple(t.shape) != (rows, heads, d):
+        raise ValueError(f"{name}: expected CUDA {_BF16} {(rows, heads, d)}, got {t.dtype} {tuple(t.shape)} "
+                         f"cuda={t.is_cuda}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
     row, head, col = t.stride()
-    if col != 1 or (heads > 1 and head != d):
+    if rows > 0 and heads > 0 and (col != 1 or (heads > 1 and head != d)):
         raise ValueError(f"{name}: expected each token's {heads} x {d} elements contiguous, got strides {t.stride()}")
-    _on_current_device(t, name)
-    return row if t.shape[0] > 1 else max(row, heads * d) // 8 * 8
+    return row if rows > 1 else heads * d
+
+
+def _rows_of(t: torch.Tensor, name: str):
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected a [T, heads, d] tensor")
+    return t.shape
 
 
 def _on_stream(stream):
-    """The context in which to allocate for a call on `stream` (None: the current one)."""
-    if stream is None:
-        return contextlib.nullcontext()
+    """The context in which to allocate for a call on `stream`."""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
 
 
-def _same_device(cache: PagedCache, batch: PagedBatch):
-    cur = torch.cuda.current_device()
-    for x, name in ((cache, "cache"), (batch, "batch")):
-        if x.device.index != cur:
-            raise ValueError(f"{name}: on {x.device}, but the current device is cuda:{cur}")
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on `stream` (None: the current one), whose memory that stream reuses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _same_device(cache: PagedCache, batch: PagedBatch) -> int:
+    """The current device, which the cache and the batch have to be on."""
+    if not torch.cuda.is_initialized():
+        raise ValueError("expected CUDA tensors")
+    cur = torch._C._cuda_getDevice()
+    if cache.device.index != cur or batch.device.index != cur:
+        raise ValueError(f"cache on {cache.device}, batch on {batch.device}, but the current device is cuda:{cur}")
+    return cur
 
 
 def fa_cache_append(k, v, cache: PagedCache, batch: PagedBatch, cos=None, sin=None, interleaved: bool = False,
@@ -322,37 +334,39 @@ def fa_cache_append(k, v, cache: PagedCache, batch: PagedBatch, cos=None, sin=No
     to the cache.  cos, sin fp32 [positions, rot / 2] rotate the keys, and the queries q (bf16 [T, Hq, d])
     into q_out (new, given, or q itself), by the tokens' positions: pairs (i, i + rot/2), or (2i, 2i + 1)
     when interleaved.  Returns the rotated queries (None without q)."""
-    T = int(k.shape[0])
-    ldk = _need_rows(k, "k", cache.heads, cache.d)
-    ldv = _need_rows(v, "v", cache.heads, cache.d, T)
-    _same_device(cache, batch)
+    T, heads, d = _rows_of(k, "k")[0], cache.heads, cache.d
+    cur = _same_device(cache, batch)
+    ldk = _need_rows(k, "k", heads, d, T, cur)
+    ldv = _need_rows(v, "v", heads, d, T, cur)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin belong together")
-    rot = n_pos = 0
+    rot = n_pos = ldq = ldqo = Hq = 0
     if cos is not None:
         if cos.dim() != 2:
             raise ValueError("cos: expected [positions, rot / 2]")
-        n_pos, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
-        if rot == 0 or rot > cache.d or rot % 16:
-            raise ValueError(f"cos, sin turn {rot} of {cache.d} columns: expected a multiple of 16, at most {cache.d}")
-        _need(cos, "cos", torch.float32, (n_pos, rot // 2))
-        _need(sin, "sin", torch.float32, (n_pos, rot // 2))
-    ldq = ldqo = Hq = 0
+        n_pos, half = cos.shape
+        rot = 2 * half
+        if rot == 0 or rot > d or rot % 16:
+            raise ValueError(f"cos, sin turn {rot} of {d} columns: expected a multiple of 16, at most {d}")
+        for t, nm in ((cos, "cos"), (sin, "sin")):
+            if t.dtype != torch.float32 or t.shape != cos.shape or not t.is_contiguous() or t.get_device() != cur:
+                _need(t, nm, torch.float32, (n_pos, half))
     if q is not None:
         if rot == 0:
             raise ValueError("q is given to be rotated: it needs cos and sin")
-        Hq = int(q.shape[1]) if q.dim() == 3 else -1
-        ldq = _need_rows(q, "q", Hq, cache.d, T)
-        if cache.heads == 0 or Hq % cache.heads:
-            raise ValueError(f"q: {Hq} heads over {cache.heads} key/value heads")
+        Hq = _rows_of(q, "q")[1]
+        ldq = _need_rows(q, "q", Hq, d, T, cur)
+        if heads == 0 or Hq % heads:
+            raise ValueError(f"q: {Hq} heads over {heads} key/value heads")
         if q_out is None:
-            with _on_stream(stream):
-                q_out = torch.empty((T, Hq, cache.d), dtype=_BF16, device=q.device)
-        ldqo = _need_rows(q_out, "q_out", Hq, cache.d, T)
+            q_out = _empty((T, Hq, d), _BF16, q.device, stream)
+            ldqo = Hq * d
+        else:
+            ldqo = _need_rows(q_out, "q_out", Hq, d, T, cur)
     elif q_out is not None:
         raise ValueError("q_out is given without q")
-    check(_lib.lib().fa_cache_append(cache._ref, batch._ref, T, _ptr(k), ldk, _ptr(v), ldv, _ptr(q), ldq,
-                                     _ptr(q_out), ldqo, Hq, _ptr(cos), _ptr(sin), rot, int(bool(interleaved)),
+    check(_lib.lib().fa_cache_append(cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(q), ldq,
+                                     _ptr(q_out), ldqo, Hq, _ptr(cos), _ptr(sin), rot, 1 if interleaved else 0,
                                      n_pos, _stream(stream)), "fa_cache_append")
     return q_out
 
@@ -367,25 +381,31 @@ def fa_fwd_paged(q, cache: PagedCache, batch: PagedBatch, scale: float | None = 
     their sequences in the cache: single tokens, a few, prompt chunks, or a mixture.  causal: token i of
     n new ones sees its sequence's keys but the last n - 1 - i.  A row that sees no key gets O = 0,
     LSE = -inf; rows behind the batch's last are left as they were."""
-    T, Hq = int(q.shape[0]), int(q.shape[1]) if q.dim() == 3 else -1
-    ldq = _need_rows(q, "q", Hq, cache.d)
+    T, Hq, _ = _rows_of(q, "q")
+    cur, d = _same_device(cache, batch), cache.d
+    ldq = _need_rows(q, "q", Hq, d, T, cur)
     if cache.heads == 0 or Hq % cache.heads:
         raise ValueError(f"q: {Hq} heads over {cache.heads} key/value heads")
-    _same_device(cache, batch)
-    scale = 1.0 / math.sqrt(cache.d) if scale is None else float(scale)
-    ws_bytes = fa_fwd_paged_workspace_size(cache, batch, T, Hq)
-    if out is None or lse is None or workspace is None:
-        with _on_stream(stream):
-            out = torch.empty((T, Hq, cache.d), dtype=_BF16, device=q.device) if out is None else out
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-            if workspace is None:
-                workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
-    _need(out, "out", _BF16, (T, Hq, cache.d))
-    _need(lse, "lse", torch.float32, (T, Hq))
-    _need_workspace(workspace, ws_bytes)
-    check(_lib.lib().fa_fwd_paged(_ptr(q), ldq, cache._ref, batch._ref, T, _ptr(out), _ptr(lse), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), Hq, scale, int(bool(causal)),
-                                  _stream(stream)), "fa_fwd_paged")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = _lib.lib()
+    ws_bytes = lib.fa_fwd_paged_workspace_size(cache._ref, batch._ref, T, Hq)
+    if workspace is None:
+        workspace = _empty((max(ws_bytes, 16),), torch.uint8, q.device, stream)
+        ws_bytes = max(ws_bytes, 16)
+    else:
+        _need_workspace(workspace, ws_bytes)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if out is None:
+        out = _empty((T, Hq, d), _BF16, q.device, stream)
+    else:
+        _need(out, "out", _BF16, (T, Hq, d))
+    if lse is None:
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
+    else:
+        _need(lse, "lse", torch.float32, (T, Hq))
+    check(lib.fa_fwd_paged(q.data_ptr(), ldq, cache._ref, batch._ref, T, out.data_ptr(), lse.data_ptr(),
+                           workspace.data_ptr(), ws_bytes, Hq, scale, 1 if causal else 0, _stream(stream)),
+          "fa_fwd_paged")
     return out, lse
 
 

@@ -10,7 +10,11 @@
 // new tokens and growing it touches all its earlier ones; the G query heads of that head ride along and
 // reuse the angles.  A thread holds 8 columns (16 bytes) of ITEMS tokens; a pair's other half is in
 // another lane of the same warp (a row is D / 8 consecutive lanes) and comes by shuffle, so every input is
-// read once and Q may be rotated in place.  Bound by HBM: it reads each row once, writes it once.
+// read once and Q may be rotated in place.  What a block waits for is two dependent loads, the batch's
+// indices and then everything else at once (keys, values, angles, four query heads and the page number);
+// the rotated keys are not kept but rotated again after the maximum, which keeps four blocks on an SM.
+// One or two new tokens a sequence (a decode batch) take blocks of one warp.  Bound by HBM for prompts
+// (each row is read once and written once), by the two loads' latency for single tokens.
 #pragma once
 
 #include "fa_paged.cuh"
@@ -102,6 +106,7 @@ __device__ __forceinline__ float amax8(const float (&x)[8], float m) {
 
 // Earlier codes of a page and head, `n` bytes (a multiple of 16), times ratio (below 1).
 __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float ratio, int t, int threads) {
+#pragma unroll 4
   for (int i = t * 16; i < n; i += threads * 16) {
     uint4 v = *reinterpret_cast<uint4*>(codes + i);
     uint32_t* w = reinterpret_cast<uint32_t*>(&v);
@@ -118,11 +123,13 @@ __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float ratio
 }
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendQ = 4;  // query heads whose rows are loaded together
 
-template <int D, bool FP8, int ITEMS>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams prm) {
+template <int D, bool FP8, int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS == 1 ? 4 : 1)
+    append_kernel(const AppendParams prm) {
   constexpr int VPR = D / 8;
-  constexpr int ROWS = kAppendThreads / VPR;  // tokens of a page the block takes at a time
+  constexpr int ROWS = THREADS / VPR;  // tokens of a page the block takes at a time
   const PagedBatch& pb = prm.b;
   const int h = blockIdx.x % pb.Hkv;
   const int unit = blockIdx.x / pb.Hkv;
@@ -137,35 +144,42 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int block = (start >> pb.page_shift) + ordinal;
   const int base = block << pb.page_shift;  // position of the page's first slot
   if (base >= s.len) return;
-  const int page = load_page(pb, b, block);
-  if (page < 0) return;
-  const int page_size = 1 << pb.page_shift;
-  const int first = max(start, base) - base, last = min(s.len, base + page_size) - base;  // slots [first, last)
-  const int vec = threadIdx.x % VPR, slot0 = threadIdx.x / VPR;
-  const size_t head_at = (static_cast<size_t>(page) * pb.Hkv + h) << pb.page_shift;  // row of slot 0 in the cache
+  const int page = pb.table[static_cast<size_t>(b) * pb.max_pages + block];  // checked below, with the loads under way
+  const int first = max(start, base) - base, last = min(s.len, base + (1 << pb.page_shift)) - base;  // slots [first, last)
+  const int vec = threadIdx.x % VPR, slot0 = first + threadIdx.x / VPR;
+  const size_t row0 = static_cast<size_t>(s.row0 + base + slot0 - start);  // this thread's first token row
 
-  uint4 kraw[ITEMS], vraw[ITEMS];
-  float kx[ITEMS][8];
-  float c[ITEMS][8], sn[ITEMS][8];
-  bool live[ITEMS];
+  uint4 kraw[ITEMS], vraw[ITEMS], qraw[kAppendQ];
+  auto live = [&](int i) { return slot0 + i * ROWS < last && (prm.rot == 0 || base + slot0 + i * ROWS < prm.n_pos); };
+  auto load_q = [&](int i, int g0) {
+#pragma unroll
+    for (int g = 0; g < kAppendQ; ++g)
+      qraw[g] = live(i) && g0 + g < prm.G
+                    ? *reinterpret_cast<const uint4*>(prm.Q + (row0 + i * ROWS) * prm.ldq + (h * prm.G + g0 + g) * D + vec * 8)
+                    : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto angles = [&](int i, float (&c)[8], float (&sn)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = sn[j] = 0.0f;
+    if (live(i) && vec * 8 < prm.rot) load_angles(prm, base + slot0 + i * ROWS, vec, c, sn);
+  };
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int slot = slot0 + i * ROWS;
-    live[i] = slot >= first && slot < last;
-    if (live[i] && prm.rot > 0 && base + slot >= prm.n_pos) {
-      live[i] = false;
-      record(pb.status, kBadPosition);
-    }
     kraw[i] = vraw[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[i][j] = sn[i][j] = 0.0f;
-    if (live[i]) {
-      const size_t row = static_cast<size_t>(s.row0 + base + slot - start);
-      kraw[i] = *reinterpret_cast<const uint4*>(prm.K + row * prm.ldk + h * D + vec * 8);
-      vraw[i] = *reinterpret_cast<const uint4*>(prm.V + row * prm.ldv + h * D + vec * 8);
-      if (vec * 8 < prm.rot) load_angles(prm, base + slot, vec, c[i], sn[i]);
+    if (live(i)) {
+      kraw[i] = *reinterpret_cast<const uint4*>(prm.K + (row0 + i * ROWS) * prm.ldk + h * D + vec * 8);
+      vraw[i] = *reinterpret_cast<const uint4*>(prm.V + (row0 + i * ROWS) * prm.ldv + h * D + vec * 8);
     }
+    if (prm.rot > 0 && slot0 + i * ROWS < last && base + slot0 + i * ROWS >= prm.n_pos) record(pb.status, kBadPosition);
   }
+  float c[8], sn[8];
+  angles(0, c, sn);
+  load_q(0, 0);
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(pb.num_pages)) {
+    record(pb.status, kBadPage);
+    return;
+  }
+  const size_t head_at = (static_cast<size_t>(page) * pb.Hkv + h) << pb.page_shift;  // row of slot 0 in the cache
   float ak = 0.0f, av = 0.0f;
   float ks_old = 0.0f, vs_old = 0.0f;
   if (FP8 && first > 0) {
@@ -174,46 +188,53 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    rotate8<D>(kraw[i], kx[i], c[i], sn[i], vec, prm.rot, prm.interleaved);
+    if (i > 0) {
+      angles(i, c, sn);
+      load_q(i, 0);
+    }
+    float x[8];
+    rotate8<D>(kraw[i], x, c, sn, vec, prm.rot, prm.interleaved);
     if constexpr (FP8) {
+      ak = amax8(x, ak);
       float vx[8];
-      rotate8<D>(vraw[i], vx, c[i], sn[i], vec, 0, 0);
-      ak = amax8(kx[i], ak);
+      rotate8<D>(vraw[i], vx, c, sn, vec, 0, 0);
       av = amax8(vx, av);
-    } else if (live[i]) {
+    } else if (live(i)) {
       const size_t at = (head_at + slot0 + i * ROWS) * D + vec * 8;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Kc) + at) = pack8_bf16(kx[i]);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Kc) + at) = pack8_bf16(x);
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Vc) + at) = vraw[i];
     }
-  }
+    for (int g0 = 0; g0 < prm.G; g0 += kAppendQ) {
+      if (g0 > 0) load_q(i, g0);
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const size_t row = static_cast<size_t>(s.row0 + base + slot0 + i * ROWS - start);
-    for (int g = 0; g < prm.G; ++g) {
-      const int col = (h * prm.G + g) * D + vec * 8;
-      uint4 qraw = make_uint4(0u, 0u, 0u, 0u);
-      if (live[i]) qraw = *reinterpret_cast<const uint4*>(prm.Q + row * prm.ldq + col);
-      float qx[8];
-      rotate8<D>(qraw, qx, c[i], sn[i], vec, prm.rot, prm.interleaved);
-      if (live[i]) *reinterpret_cast<uint4*>(prm.Qo + row * prm.ldqo + col) = pack8_bf16(qx);
+      for (int g = 0; g < kAppendQ; ++g) {
+        rotate8<D>(qraw[g], x, c, sn, vec, prm.rot, prm.interleaved);
+        if (live(i) && g0 + g < prm.G)
+          *reinterpret_cast<uint4*>(prm.Qo + (row0 + i * ROWS) * prm.ldqo + (h * prm.G + g0 + g) * D + vec * 8) =
+              pack8_bf16(x);
+      }
     }
   }
   if constexpr (FP8) {
-    __shared__ float red[2][kAppendThreads / 32];
+    __shared__ float red[2][THREADS / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
       av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
     }
-    if ((threadIdx.x & 31) == 0) {
-      red[0][threadIdx.x >> 5] = ak;
-      red[1][threadIdx.x >> 5] = av;
-    }
-    __syncthreads();  // also: every thread has read the old scales
+    if (THREADS > 32) {
+      if ((threadIdx.x & 31) == 0) {
+        red[0][threadIdx.x >> 5] = ak;
+        red[1][threadIdx.x >> 5] = av;
+      }
+      __syncthreads();  // also: every thread has read the old scales
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) {
-      ak = fmaxf(ak, red[0][w]);
-      av = fmaxf(av, red[1][w]);
+      for (int w = 0; w < THREADS / 32; ++w) {
+        ak = fmaxf(ak, red[0][w]);
+        av = fmaxf(av, red[1][w]);
+      }
+    } else {
+      __syncwarp();
     }
     const float ks = fmaxf(ks_old, needed_scale(ak)), vs = fmaxf(vs_old, needed_scale(av));
     uint8_t* kc = static_cast<uint8_t*>(prm.Kc) + head_at * D;
@@ -222,16 +243,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       prm.Ks[static_cast<size_t>(page) * pb.Hkv + h] = ks;
       prm.Vs[static_cast<size_t>(page) * pb.Hkv + h] = vs;
     }
-    if (first > 0 && ks > ks_old) rescale_codes(kc, first * D, ks_old / ks, threadIdx.x, kAppendThreads);
-    if (first > 0 && vs > vs_old) rescale_codes(vc, first * D, vs_old / vs, threadIdx.x, kAppendThreads);
+    if (first > 0 && ks > ks_old) rescale_codes(kc, first * D, ks_old / ks, threadIdx.x, THREADS);
+    if (first > 0 && vs > vs_old) rescale_codes(vc, first * D, vs_old / vs, threadIdx.x, THREADS);
     const float ki = 1.0f / ks, vi = 1.0f / vs;  // exact for the powers of two written here
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      if (!live[i]) continue;
+      if (ITEMS > 1) angles(i, c, sn);
+      float x[8], vx[8];
+      rotate8<D>(kraw[i], x, c, sn, vec, prm.rot, prm.interleaved);
+      rotate8<D>(vraw[i], vx, c, sn, vec, 0, 0);
+      if (!live(i)) continue;
       const size_t at = static_cast<size_t>(slot0 + i * ROWS) * D + vec * 8;
-      float vx[8];
-      rotate8<D>(vraw[i], vx, c[i], sn[i], vec, 0, 0);
-      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(kx[i], ki);
+      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(x, ki);
       *reinterpret_cast<uint2*>(vc + at) = pack8_e4m3(vx, vi);
     }
   }

@@ -113,15 +113,17 @@ bool make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache* c, 
 }
 
 template <int D, bool FP8>
-int launch_append(const fa::AppendParams& prm, long long grid, cudaStream_t st) {
-  const int items = max(1, (1 << prm.b.page_shift) * (D / 8) / fa::kAppendThreads);
+int launch_append(const fa::AppendParams& prm, long long grid, int most, cudaStream_t st) {
+  constexpr int N = fa::kAppendThreads, VPR = D / 8;
   const unsigned g = static_cast<unsigned>(grid);
-  switch (items) {
-    case 1: fa::append_kernel<D, FP8, 1><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
-    case 2: fa::append_kernel<D, FP8, 2><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
-    case 4: fa::append_kernel<D, FP8, 4><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
-    default: fa::append_kernel<D, FP8, 8><<<g, fa::kAppendThreads, 0, st>>>(prm); break;
-  }
+  // new tokens that a page can get, by the rows a block takes at a time
+  const int rows = most < (1 << prm.b.page_shift) ? most : 1 << prm.b.page_shift;
+  const int items = (rows + N / VPR - 1) / (N / VPR);
+  if (rows <= 32 / VPR) fa::append_kernel<D, FP8, 32, 1><<<g, 32, 0, st>>>(prm);
+  else if (items <= 1) fa::append_kernel<D, FP8, N, 1><<<g, N, 0, st>>>(prm);
+  else if (items <= 2) fa::append_kernel<D, FP8, N, 2><<<g, N, 0, st>>>(prm);
+  else if (items <= 4) fa::append_kernel<D, FP8, N, 4><<<g, N, 0, st>>>(prm);
+  else fa::append_kernel<D, FP8, N, 8><<<g, N, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -269,8 +271,8 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
   if (grid > INT_MAX) return FA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache->type == FA_CACHE_E4M3;
-  if (d == 128) return fp8 ? launch_append<128, true>(prm, grid, st) : launch_append<128, false>(prm, grid, st);
-  return fp8 ? launch_append<64, true>(prm, grid, st) : launch_append<64, false>(prm, grid, st);
+  if (d == 128) return fp8 ? launch_append<128, true>(prm, grid, most, st) : launch_append<128, false>(prm, grid, most, st);
+  return fp8 ? launch_append<64, true>(prm, grid, most, st) : launch_append<64, false>(prm, grid, most, st);
 }
 
 size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, int Hq) {
@@ -312,8 +314,8 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   FwdMaps m;
   const int box = cache->page_size < tile ? cache->page_size : tile;
   if (!make_page_map(&m.dec_k, cache->K, cache, box) || !make_page_map(&m.dec_v, cache->V, cache, box) ||
-      !make_page_map(&m.pre_k, cache->K, cache, cache->page_size) ||
-      !make_page_map(&m.pre_v, cache->V, cache, cache->page_size))
+      (many && (!make_page_map(&m.pre_k, cache->K, cache, cache->page_size) ||
+                !make_page_map(&m.pre_v, cache->V, cache, cache->page_size))))
     return FA_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   fa::DecodeParams dec;
