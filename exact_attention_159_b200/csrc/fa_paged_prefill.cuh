@@ -51,7 +51,7 @@ struct PrefillParams {
 template <int D, bool FP8>
 struct PrefillLayout {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kRawBytes = FP8 ? kTile * D : 0;  // e4m3 staging of one tile
+  static constexpr int kRawBytes = FP8 ? kTile * D : 0;  // e4m3 staging of one tile, in two halves of 64 keys
   static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + 2 * kTileBytes;
@@ -61,9 +61,11 @@ struct PrefillLayout {
   static constexpr int kMeta = kRawV + kRawBytes;  // [8 tiles][8 groups of 16 keys] page_scales
   static constexpr int kBar = kMeta + (FP8 ? 8 * 8 * 16 : 0);
   // q_full[2], k_full[S], v_full[S], k_empty[S], v_empty[S], v_land[S], s_full[2], p_full[2], o_full[2], drain,
-  // kraw_full, kraw_empty, vraw_full, vraw_empty
-  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 4;
-  static constexpr int kMisc = kBar + kNumBars * 8;
+  // kraw_full[2], kraw_empty[2], vraw_full[2], vraw_empty[2], seg_full[kSegs], seg_empty[kSegs]
+  static constexpr int kSegs = 4;
+  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 8 + 2 * kSegs;
+  static constexpr int kSeg = kBar + kNumBars * 8 + (kNumBars & 1) * 8;
+  static constexpr int kMisc = kSeg + kSegs * 48;
   static constexpr int kBytes = kMisc + 16 + 16 * 8;
   static constexpr int kThreads = 384;
   static constexpr int kLaunchRegs = (65536 / kThreads) / 8 * 8;
@@ -260,6 +262,17 @@ struct PrefillWalk {
   }
 };
 
+// A segment as the producer publishes it to the other warps.
+struct alignas(16) PrefillSegment {
+  int row0, rows, len;  // the sequence
+  int h, p;             // key/value head, pair of query tiles
+  int t0;               // first key tile; below 0: the share is done
+  int end[2];           // the first one that each query tile does not see
+  int whole;            // the item is whole: results, not parts
+  int pad[3];
+};
+static_assert(sizeof(PrefillSegment) == 48, "segment slots are 48 bytes");
+
 // --------------------------------------------------------------------------------------- kernel
 template <int D, bool FP8>
 __global__ void __launch_bounds__(384, 1)
@@ -286,9 +299,12 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* o_full = p_full + 2;
   uint64_t* drain = o_full + 2;
   uint64_t* kraw_full = drain + 1;
-  uint64_t* kraw_empty = kraw_full + 1;
-  uint64_t* vraw_full = kraw_empty + 1;
-  uint64_t* vraw_empty = vraw_full + 1;
+  uint64_t* kraw_empty = kraw_full + 2;
+  uint64_t* vraw_full = kraw_empty + 2;
+  uint64_t* vraw_empty = vraw_full + 2;
+  uint64_t* seg_full = vraw_empty + 2;
+  uint64_t* seg_empty = seg_full + L::kSegs;
+  PrefillSegment* segs = reinterpret_cast<PrefillSegment*>(smem + L::kSeg);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   int* abort_flag = reinterpret_cast<int*>(smem + L::kMisc + 4);
   long long* scratch = reinterpret_cast<long long*>(smem + L::kMisc + 16);
@@ -310,7 +326,13 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&p_full[t], 128);
       mbar_init(&o_full[t], 1);
     }
-    for (uint64_t* b : {drain, kraw_full, kraw_empty, vraw_full, vraw_empty}) mbar_init(b, 1);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i)
+      for (uint64_t* b : {kraw_full, kraw_empty, vraw_full, vraw_empty}) mbar_init(b + i, 1);
+    for (int i = 0; i < L::kSegs; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 11);  // the MMA thread, warps 2 and 3, eight softmax warps
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -323,8 +345,21 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Guard g{abort_flag, prm.b.status};
-  PrefillWalk w;
-  w.start(prm, share, blockIdx.x);
+  // The producer walks the share and publishes its segments; the others read them, each in turn.
+  int seg_n = 0;
+  auto segment = [&](bool& ok, auto whole_warp) -> const PrefillSegment* {  // null: the share is done, or a wait failed
+    const int i = seg_n % L::kSegs;
+    const uint32_t ph = (seg_n / L::kSegs) & 1;
+    ok = decltype(whole_warp)::value ? wait_warp(&seg_full[i], ph, g, kSitePrefill | 15)
+                                     : wait(&seg_full[i], ph, g, kSitePrefill | 15);
+    return !ok || segs[i].t0 < 0 ? nullptr : &segs[i];
+  };
+  constexpr std::true_type kWarp{};
+  constexpr std::false_type kThread{};
+  auto segment_done = [&](bool arrives) {  // this thread (or warp) has read all it needs of the segment
+    if (arrives) mbar_arrive(&seg_empty[seg_n % L::kSegs]);
+    ++seg_n;
+  };
 
   if (warp < 4) {
     regs_to<kFwdRegsCtl, L::kLaunchRegs>();
@@ -333,58 +368,103 @@ __global__ void __launch_bounds__(384, 1)
       // Lane i issues the boxes of a tile's i-th page.
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
-      const int shift = min(prm.b.page_shift, 7), box_rows = 1 << shift;
+      PrefillWalk w;
+      w.start(prm, share, blockIdx.x);
+      const int shift = min(prm.b.page_shift, FP8 ? 6 : 7), box_rows = 1 << shift;  // e4m3 lands in halves of 64 keys
       constexpr int kCols = FP8 ? D : 64;
-      bool ok = true;
-      int kt = 0, k_issued = 0, v_issued = 0;  // key tiles since the start
-      do {
-        const int end = max(w.end(prm, 0), w.end(prm, 1));
+      bool ok = true, more = true;
+      int kt = 0;                      // key tiles since the start
+      int kn[2] = {0, 0}, vn[2] = {0, 0};  // loads issued (e4m3: of each half; bf16: [0])
+      while (ok) {
+        const int si = seg_n % L::kSegs;
+        if (!(ok = wait_warp(&seg_empty[si], ((seg_n / L::kSegs) & 1) ^ 1, g, kSitePrefill | 16))) break;
+        ++seg_n;
+        const int end = more ? max(w.end(prm, 0), w.end(prm, 1)) : 0;
+        if (lane == 0) {
+          PrefillSegment& x = segs[si];
+          x.row0 = w.d.s.row0;
+          x.rows = w.d.s.rows;
+          x.len = w.d.s.len;
+          x.h = w.h;
+          x.p = w.p;
+          x.t0 = more ? w.t0 : -1;
+          x.end[0] = w.end(prm, 0);
+          x.end[1] = w.end(prm, 1);
+          x.whole = w.whole;
+          mbar_arrive(&seg_full[si]);
+        }
+        if (!more) break;
         for (int j = w.t0; j < end && ok; ++j, ++kt) {
           const int keys = min(kTile, w.d.s.len - j * kTile);
           const int boxes = (keys + box_rows - 1) >> shift;
-          const int first_page = (j * kTile) >> prm.b.page_shift;
-          int z = 0;
+          int z = 0, y = 0;
           float4 sc = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
           if (lane < boxes) {
-            const int page = load_page(prm.b, w.b, first_page + lane);
+            const int key = j * kTile + (lane << shift);
+            const int page = load_page(prm.b, w.b, key >> prm.b.page_shift);
             // a page out of range reads as zeros beyond the map's last head
             z = page >= 0 ? page * prm.b.Hkv + w.h : prm.b.num_pages * prm.b.Hkv;
-            if (FP8 && page >= 0)
-              sc = page_scales(prm.Ks[z], prm.Vs[z]);
+            y = key & ((1 << prm.b.page_shift) - 1);
+            if (FP8 && page >= 0) sc = page_scales(prm.Ks[z], prm.Vs[z]);
           }
-          const int s = kt % S;
-          const uint32_t ph = (kt / S) & 1;
-          uint64_t* full = FP8 ? kraw_full : &k_full[s];
-          ok = wait_warp(FP8 ? kraw_empty : &k_empty[s], FP8 ? (kt & 1) ^ 1 : ph ^ 1, g, kSitePrefill | 1);
-          if (!ok) break;
-          if (FP8 && lane < boxes) {
-            // the scales of the page's groups of 16 keys; of the eight slots the one written here was last
-            // read for tile kt - 8, and the S that the operand ring has already seen done come after that
-            float4* m = reinterpret_cast<float4*>(smem + L::kMeta) + (kt & 7) * 8 + (lane << (shift - 4));
-            for (int i = 0; i < 1 << (shift - 4); ++i) m[i] = sc;
+          if constexpr (FP8) {
+            // two halves of 64 keys each, K's then V's: a half's slot is free once its codes are halves
+            const int per_half = 64 >> shift;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int n = min(boxes - hf * per_half, per_half);
+              if (n <= 0) break;
+              const bool mine = lane >= hf * per_half && lane < hf * per_half + n;
+              const int bytes = n * box_rows * D, at = lane * box_rows * D;
+              if (!(ok = wait_warp(&kraw_empty[hf], (kn[hf] & 1) ^ 1, g, kSitePrefill | 1))) break;
+              ++kn[hf];
+              if (mine) {
+                // the scales of the page's groups of 16 keys; of the eight slots the one written here was last
+                // read for tile kt - 8, and the S that the operand ring has already seen done come after that
+                float4* m = reinterpret_cast<float4*>(smem + L::kMeta) + (kt & 7) * 8 + (lane << (shift - 4));
+                for (int i = 0; i < 1 << (shift - 4); ++i) m[i] = sc;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_expect_tx(&kraw_full[hf], bytes);
+              __syncwarp();
+              if (mine) tma_load_3d(smem + L::kRawK + at, &tmK, 0, y, z, &kraw_full[hf]);
+              if (!(ok = wait_warp(&vraw_empty[hf], (vn[hf] & 1) ^ 1, g, kSitePrefill | 2))) break;
+              ++vn[hf];
+              if (lane == 0) mbar_expect_tx(&vraw_full[hf], bytes);
+              __syncwarp();
+              if (mine) tma_load_3d(smem + L::kRawV + at, &tmV, 0, y, z, &vraw_full[hf]);
+            }
+          } else {
+            const int s = kt % S, bytes = boxes * box_rows * D * 2;
+            const uint32_t ph = (kt / S) & 1;
+            if (!(ok = wait_warp(&k_empty[s], ph ^ 1, g, kSitePrefill | 1))) break;
+            if (lane == 0) mbar_expect_tx(&k_full[s], bytes);
+            __syncwarp();
+            if (lane < boxes)
+              for (int c = 0; c < D / kCols; ++c)
+                tma_load_3d(smem + L::kK + s * T + c * 16384 + lane * box_rows * 128, &tmK, c * kCols, y, z, &k_full[s]);
+            ++kn[0];
+            if (!(ok = wait_warp(&v_empty[s], ph ^ 1, g, kSitePrefill | 2))) break;
+            if (lane == 0) mbar_expect_tx(&v_land[s], bytes);
+            __syncwarp();
+            if (lane < boxes)
+              for (int c = 0; c < D / kCols; ++c)
+                tma_load_3d(smem + L::kV + s * T + c * 16384 + lane * box_rows * 128, &tmV, c * kCols, y, z, &v_land[s]);
+            ++vn[0];
           }
-          __syncwarp();
-          const int bytes = boxes * box_rows * D * (FP8 ? 1 : 2);
-          if (lane == 0) mbar_expect_tx(full, bytes);
-          __syncwarp();
-          uint8_t* to = smem + (FP8 ? L::kRawK : L::kK + s * T) + lane * box_rows * kCols * (FP8 ? 1 : 2);
-          if (lane < boxes)
-            for (int c = 0; c < D / kCols; ++c) tma_load_3d(to + c * 16384, &tmK, c * kCols, 0, z, full);
-          ++k_issued;
-          full = FP8 ? vraw_full : &v_land[s];
-          if (!(ok = wait_warp(FP8 ? vraw_empty : &v_empty[s], FP8 ? (kt & 1) ^ 1 : ph ^ 1, g, kSitePrefill | 2))) break;
-          if (lane == 0) mbar_expect_tx(full, bytes);
-          __syncwarp();
-          to = smem + (FP8 ? L::kRawV : L::kV + s * T) + lane * box_rows * kCols * (FP8 ? 1 : 2);
-          if (lane < boxes)
-            for (int c = 0; c < D / kCols; ++c) tma_load_3d(to + c * 16384, &tmV, c * kCols, 0, z, full);
-          ++v_issued;
         }
-      } while (ok && w.next(prm));
+        if (ok) more = w.next(prm);
+      }
       if (!ok) {  // let copies already in flight land before the CTA exits
-        constexpr int R = FP8 ? 1 : S;
-        for (int i = max(k_issued - R, 0); i < k_issued; ++i) drain_wait(FP8 ? kraw_full : &k_full[i % R], (i / R) & 1);
-        for (int i = max(v_issued - R, 0); i < v_issued; ++i) drain_wait(FP8 ? vraw_full : &v_land[i % R], (i / R) & 1);
+        if constexpr (FP8) {
+          for (int hf = 0; hf < 2; ++hf) {
+            if (kn[hf] > 0) drain_wait(&kraw_full[hf], (kn[hf] - 1) & 1);
+            if (vn[hf] > 0) drain_wait(&vraw_full[hf], (vn[hf] - 1) & 1);
+          }
+        } else {
+          for (int i = max(kn[0] - S, 0); i < kn[0]; ++i) drain_wait(&k_full[i % S], (i / S) & 1);
+          for (int i = max(vn[0] - S, 0); i < vn[0]; ++i) drain_wait(&v_land[i % S], (i / S) & 1);
+        }
       }
     } else if (warp == 1) {
       // --------------------------------------------------------------------------------- MMA
@@ -410,13 +490,14 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = true;
         int kt = 0;
         int qn[2] = {0, 0}, steps[2] = {0, 0};  // query tiles loaded, tile steps done
-        do {
-          const int end[2] = {w.end(prm, 0), w.end(prm, 1)};
+        while (const PrefillSegment* w = segment(ok, kThread)) {
+          const int t0 = w->t0, end[2] = {w->end[0], w->end[1]};
           const int last = max(end[0], end[1]);
-          if (last == w.t0) continue;
+          segment_done(true);
+          if (last == t0) continue;
           if (!(ok = wait(&k_full[kt % S], (kt / S) & 1, g, kSitePrefill | 3))) break;
           for (int t = 0; t < 2 && ok; ++t)
-            if (end[t] > w.t0) {
+            if (end[t] > t0) {
               if (!(ok = wait(&q_full[t], qn[t]++ & 1, g, kSitePrefill | 4))) break;
               tc_fence_after();
               issue_s(t, kt % S);
@@ -424,14 +505,14 @@ __global__ void __launch_bounds__(384, 1)
             }
           if (!ok) break;
           tc_commit(&k_empty[kt % S]);
-          for (int j = w.t0; ok && j < last; ++j, ++kt) {
+          for (int j = t0; ok && j < last; ++j, ++kt) {
             const int s = kt % S, s1 = (kt + 1) % S;
             if (!(ok = wait(&v_full[s], (kt / S) & 1, g, kSitePrefill | 5))) break;
             for (int t = 0; t < 2 && ok; ++t) {
               if (j >= end[t]) continue;
               if (!(ok = wait(&p_full[t], steps[t]++ & 1, g, kSitePrefill | 7))) break;
               tc_fence_after();
-              issue_pv(t, s, j > w.t0);
+              issue_pv(t, s, j > t0);
               tc_commit(&o_full[t]);
               if (j + 1 < end[t]) {
                 if (!(ok = wait(&k_full[s1], ((kt + 1) / S) & 1, g, kSitePrefill | 8))) break;
@@ -445,7 +526,8 @@ __global__ void __launch_bounds__(384, 1)
               if (j + 1 < last) tc_commit(&k_empty[s1]);
             }
           }
-        } while (ok && w.next(prm));
+          if (!ok) break;
+        }
         tc_commit(drain);
         drain_wait(drain, 0);
       }
@@ -456,57 +538,66 @@ __global__ void __launch_bounds__(384, 1)
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       const uint32_t raw = smem_u32(smem + (is_v ? L::kRawV : L::kRawK));
       bool ok = true;
-      int kt = 0;
-      do {
-        const int end = max(w.end(prm, 0), w.end(prm, 1));
-        for (int j = w.t0; j < end && ok; ++j, ++kt) {
+      int kt = 0, rn[2] = {0, 0};
+      while (const PrefillSegment* w = segment(ok, kWarp)) {
+        const int t0 = w->t0, end = max(w->end[0], w->end[1]), len = w->len;
+        __syncwarp();
+        segment_done(lane == 0);
+        for (int j = t0; j < end && ok; ++j, ++kt) {
           const int s = kt % S;
-          if (!(ok = wait_warp(rfull, kt & 1, g, kSitePrefill | 9))) break;
-          if (!(ok = wait_warp(&empty[s], ((kt / S) & 1) ^ 1, g, kSitePrefill | 10))) break;
-          const int live = w.d.s.len - j * kTile;  // rows behind it become zeros
+          const int live = len - j * kTile;  // rows behind it become zeros
           const uint32_t to = smem_u32(smem + (is_v ? L::kV : L::kK) + s * T);
           constexpr int CH = D / 16;  // 16-byte chunks of a row of codes
-          // eight lanes store rows r and r + 1 (of 4 chunks each): no two to the same bank
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            const bool loaded = hf == 0 || live > 64;
+            if (loaded && !(ok = wait_warp(&rfull[hf], rn[hf]++ & 1, g, kSitePrefill | 9))) break;
+            if (hf == 0 && !(ok = wait_warp(&empty[s], ((kt / S) & 1) ^ 1, g, kSitePrefill | 10))) break;
+            // eight lanes store rows r and r + 1 (of 4 chunks each): no two to the same bank
 #pragma unroll 4
-          for (int i = 0; i < kTile * CH / 32; ++i) {
-            int r, c;
-            if constexpr (D == 128) {
-              r = (i >> 1) * 8 + (lane >> 2), c = (lane & 3) + 4 * (i & 1);
-            } else {
-              r = i * 8 + (lane >> 2), c = lane & 3;
+            for (int i = 0; i < 64 * CH / 32; ++i) {
+              int r, c;
+              if constexpr (D == 128) {
+                r = hf * 64 + (i >> 1) * 8 + (lane >> 2), c = (lane & 3) + 4 * (i & 1);
+              } else {
+                r = hf * 64 + i * 8 + (lane >> 2), c = lane & 3;
+              }
+              const uint32_t from = D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4) : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+              uint4 x = lds128(from);
+              if (r >= live) x = make_uint4(0u, 0u, 0u, 0u);
+              uint32_t h[8];
+              halves_of_e4m3(x.x, h[0], h[1]);
+              halves_of_e4m3(x.y, h[2], h[3]);
+              halves_of_e4m3(x.z, h[4], h[5]);
+              halves_of_e4m3(x.w, h[6], h[7]);
+              const uint32_t at = to + (c >> 2) * 16384 + r * 128, c2 = 2 * (c & 3);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2) ^ (r & 7)) << 4)), "r"(h[0]),
+                           "r"(h[1]), "r"(h[2]), "r"(h[3])
+                           : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2 + 1) ^ (r & 7)) << 4)), "r"(h[4]),
+                           "r"(h[5]), "r"(h[6]), "r"(h[7])
+                           : "memory");
             }
-            const uint32_t from = D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4) : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-            uint4 x = lds128(from);
-            if (r >= live) x = make_uint4(0u, 0u, 0u, 0u);
-            uint32_t h[8];
-            halves_of_e4m3(x.x, h[0], h[1]);
-            halves_of_e4m3(x.y, h[2], h[3]);
-            halves_of_e4m3(x.z, h[4], h[5]);
-            halves_of_e4m3(x.w, h[6], h[7]);
-            const uint32_t at = to + (c >> 2) * 16384 + r * 128, c2 = 2 * (c & 3);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2) ^ (r & 7)) << 4)), "r"(h[0]),
-                         "r"(h[1]), "r"(h[2]), "r"(h[3])
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2 + 1) ^ (r & 7)) << 4)), "r"(h[4]),
-                         "r"(h[5]), "r"(h[6]), "r"(h[7])
-                         : "memory");
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[s]);
-            mbar_arrive(rempty);
+            if (hf == 1) fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (loaded) mbar_arrive(&rempty[hf]);
+              if (hf == 1) mbar_arrive(&full[s]);
+            }
           }
         }
-      } while (ok && w.next(prm));
+        if (!ok) break;
+      }
     } else if (warp == 3) {
       // ------------------------------------------- values behind a sequence's end become zeros
       bool ok = true;
       int kt = 0;
-      do {
-        const int end = max(w.end(prm, 0), w.end(prm, 1));
-        for (int j = w.t0; j < end && ok; ++j, ++kt) {
-          const int live = w.d.s.len - j * kTile, s = kt % S;
+      while (const PrefillSegment* w = segment(ok, kWarp)) {
+        const int t0 = w->t0, end = max(w->end[0], w->end[1]), len = w->len;
+        __syncwarp();
+        segment_done(lane == 0);
+        for (int j = t0; j < end && ok; ++j, ++kt) {
+          const int live = len - j * kTile, s = kt % S;
           if (!(ok = wait_warp(&v_land[s], (kt / S) & 1, g, kSitePrefill | 11))) break;
           if (live < kTile) {
             for (int i = lane; i < (kTile - live) * 8; i += 32)
@@ -519,7 +610,12 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (lane == 0) mbar_arrive(&v_full[s]);
         }
-      } while (ok && w.next(prm));
+        if (!ok) break;
+      }
+    }
+    if (!FP8 && warp == 2 && lane == 0) {  // takes part in the segments' hand-over only
+      bool ok = true;
+      while (segment(ok, kThread)) segment_done(true);
     }
   } else {
     regs_to<kFwdRegsSoftmax, L::kLaunchRegs>();
@@ -533,19 +629,17 @@ __global__ void __launch_bounds__(384, 1)
     const float4* meta = reinterpret_cast<const float4*>(smem + L::kMeta);
     bool ok = true;
     int step = 0, kt0 = 0;  // this tile's steps, key tiles of the CTA before the segment
-    do {
-      const int ends[2] = {w.end(prm, 0), w.end(prm, 1)};
-      const int end = ends[t];
-      const int row = w.p * kPreRows + t * kTile + r;  // of the sequence's rows * G
-      const bool real = row < w.d.s.rows * prm.G;
-      const int token = real ? row / prm.G : 0, head = w.h * prm.G + (real ? row % prm.G : 0);
-      const int off = w.d.s.len - w.d.s.rows;
-      const int lim = prm.causal && real ? off + token : w.d.s.len - 1;  // last visible key
-      const int lim_min = prm.causal ? off + (w.p * kPreRows + t * kTile) / prm.G : w.d.s.len - 1;
+    while (const PrefillSegment* w = segment(ok, kWarp)) {
+      const int t0 = w->t0, end = w->end[t], len = w->len;
+      // this thread's row of the sequence's rows * G: its token and query head
+      int token = (w->p * kPreRows + t * kTile + r) / prm.G, head = (w->p * kPreRows + t * kTile + r) % prm.G + w->h * prm.G;
+      const bool real = token < w->rows;
+      const int lim = prm.causal && real ? len - w->rows + token : len - 1;  // last visible key
+      const int lim_min = prm.causal ? len - w->rows + (w->p * kPreRows + t * kTile) / prm.G : len - 1;
       float sl2 = prm.scale_log2;
-      if (end > w.t0) {
+      if (end > t0) {
         // this thread's row of Q; the tile's last S is done, since this thread has seen its scores
-        const uint4* q = reinterpret_cast<const uint4*>(prm.Q + static_cast<size_t>(w.d.s.row0 + token) * prm.ldq + head * D);
+        const uint4* q = reinterpret_cast<const uint4*>(prm.Q + static_cast<size_t>(w->row0 + token) * prm.ldq + head * D);
         uint4 x[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) x[i] = real ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -578,7 +672,7 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&q_full[t]);
       }
       float m_ref = -INFINITY, l = 0.0f;
-      for (int j = w.t0; j < end; ++j, ++step) {
+      for (int j = t0; j < end; ++j, ++step) {
         if (!(ok = wait_warp(&s_full[t], step & 1, g, kSitePrefill | 12))) break;
         tc_fence_after();
         uint32_t sr[4][32];
@@ -593,7 +687,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int c = 0; c < kTile; ++c)
             if (j * kTile + c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
         }
-        const float4* mt = meta + ((kt0 + j - w.t0) & 7) * 8;
+        const float4* mt = meta + ((kt0 + j - t0) & 7) * 8;
         // row maximum (e4m3: of each group of 16 keys, then with the group's scales)
         float top;
         if constexpr (FP8) {
@@ -606,7 +700,7 @@ __global__ void __launch_bounds__(384, 1)
             m0 = fmax3(m0, S(16 * q + 10), S(16 * q + 11));
             m1 = fmax3(m1, S(16 * q + 12), S(16 * q + 13));
             m0 = fmax3(m0, S(16 * q + 14), S(16 * q + 15));
-            const bool live = j * kTile + 16 * q < w.d.s.len;  // a page behind the end brought no scales
+            const bool live = j * kTile + 16 * q < len;  // a page behind the end brought no scales
             const float4 sc = mt[q];
             // a group that is wholly masked stays at -inf whatever its scale (zero too)
             const float x = fmaxf(m0, m1);
@@ -643,7 +737,7 @@ __global__ void __launch_bounds__(384, 1)
             float inv = 1.0f;
             bool tiny = false;
             if constexpr (FP8) {
-              const bool live = j * kTile + 32 * cc + 16 * hh < w.d.s.len;
+              const bool live = j * kTile + 32 * cc + 16 * hh < len;
               const float4 sc = mt[2 * cc + hh];
               const float f = live ? fmaxf(sl2 * sc.x, 1e-37f) : 1.0f, n = live ? sc.y + sc.w - m_sub : 0.0f;
               inv = live ? sc.z : 0.0f;
@@ -676,7 +770,7 @@ __global__ void __launch_bounds__(384, 1)
 #undef S
         const float2 ls = __fadd2_rn(ls0, ls1);
         l += ls.x + ls.y;
-        if (j > w.t0 && __any_sync(0xffffffffu, need)) {
+        if (j > t0 && __any_sync(0xffffffffu, need)) {
           // O_t *= alpha once the previous P.V has landed (before p_full lets the next one add to it)
           ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 13);
           tc_fence_after();
@@ -699,19 +793,20 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
-      const size_t at = static_cast<size_t>(w.d.s.row0 + token) * prm.Hq + head;
-      const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, w.t0)) * kPreRows + t * kTile + r;
-      if (end > w.t0) {
+      const size_t at = static_cast<size_t>(w->row0 + token) * prm.Hq + head;
+      const bool whole = w->whole;
+      const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, t0)) * kPreRows + t * kTile + r;
+      if (end > t0) {
         if (!(ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 14))) break;
         tc_fence_after();
-        const float scale = !w.whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        const float scale = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
           tmem_wait_ld();
           reg_fence(o);
-          if (real && w.whole) {
+          if (real && whole) {
             uint4* dst = reinterpret_cast<uint4*>(prm.O + at * D + 32 * c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -728,16 +823,18 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         tc_fence_before();
-      } else if (real && w.whole) {  // no key is visible to any row of the tile
+      } else if (real && whole) {  // no key is visible to any row of the tile
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(prm.O + at * D)[i] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (real) {
-        if (w.whole) prm.LSE[at] = l > 0.0f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (whole) prm.LSE[at] = l > 0.0f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
         else prm.part_ml[slot] = make_float2(m_ref, l);  // m = -inf: the join takes nothing from this part
       }
-      kt0 += max(ends[0], ends[1]) - w.t0;
-    } while (w.next(prm));
+      kt0 += max(w->end[0], w->end[1]) - t0;
+      __syncwarp();
+      segment_done(lane == 0);
+    }
   }
   tc_fence_before();
   __syncthreads();
