@@ -313,9 +313,8 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   const int tile = fp8 ? fa::DecodeLayout<128, true>::kTile : fa::DecodeLayout<128, false>::kTile;
   FwdMaps m;
   const int box = cache->page_size < tile ? cache->page_size : tile;
-  const int pre_box = fp8 && cache->page_size == 128 ? 64 : cache->page_size;  // e4m3 lands in halves of a tile
   if (!make_page_map(&m.dec_k, cache->K, cache, box) || !make_page_map(&m.dec_v, cache->V, cache, box) ||
-      (many && (!make_page_map(&m.pre_k, cache->K, cache, pre_box) || !make_page_map(&m.pre_v, cache->V, cache, pre_box))))
+      (many && (!make_page_map(&m.pre_k, cache->K, cache, cache->page_size) || !make_page_map(&m.pre_v, cache->V, cache, cache->page_size))))
     return FA_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   fa::DecodeParams dec;

@@ -14,11 +14,12 @@
 //   Pages.  A 128-key tile is one TMA box for each of its pages.  Slots behind the sequence's end may hold
 //     anything: their scores are masked, and their values are zeroed in shared memory before the MMA (a
 //     weight of zero times a NaN is not zero).
-//   e4m3.  Codes land in a staging tile; two warps turn them into halves (exact) in the operand tiles, at about
-//     a quarter of the time that an iteration leaves them.  The scales stay outside the products: K's
-//     multiplies the scores of its 16 columns or more, V's joins the exponent (w = 2^(s + log2 vs - m),
-//     O = sum w * code, the softmax's sum is sum w / vs).  Q becomes halves by a power of two per row, P is
-//     rounded to half.
+//   e4m3.  S comes from the codes themselves: a row of Q, brought to 256 by a power of two, is the sum of two
+//     e4m3 rows (its 8-bit significands in two parts; what is below 2^-18 of the row's largest is rounded off),
+//     so S = Q1 K^T + Q2 K^T on the 8-bit tensor pipe, as fast as one 16-bit product and with no conversion of
+//     K.  V's codes land in a staging ring and two warps turn them into halves (exact).  The scales stay outside
+//     the products: K's multiplies the scores of its 16 columns or more, V's joins the exponent (w = 2^(s +
+//     log2 vs - m), O = sum w * code, the softmax's sum is sum w / vs).  P is rounded to half.
 #pragma once
 
 #include "exp2_poly.cuh"
@@ -50,20 +51,23 @@ struct PrefillParams {
 
 template <int D, bool FP8>
 struct PrefillLayout {
-  static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kRawBytes = FP8 ? kTile * D : 0;  // e4m3 staging of one tile, in two halves of 64 keys
-  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kQBytes = kTile * D * 2;             // a tile of Q: bf16, or two parts of e4m3
+  static constexpr int kKBytes = kTile * D * (FP8 ? 1 : 2);
+  static constexpr int kVBytes = kTile * D * 2;             // bf16 or halves
+  static constexpr int kRawBytes = FP8 ? kTile * D : 0;     // e4m3 staging of a tile of V
+  static constexpr int kStagesK = (D == 128 ? 2 : 3) + (FP8 ? 1 : 0);
+  static constexpr int kStagesV = D == 128 ? 2 : 3;
+  static constexpr int kRaws = 2;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + 2 * kTileBytes;
-  static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kRawK = kV + kStages * kTileBytes;
-  static constexpr int kRawV = kRawK + kRawBytes;
-  static constexpr int kMeta = kRawV + kRawBytes;  // [8 tiles][8 groups of 16 keys] page_scales
+  static constexpr int kK = kQ + 2 * kQBytes;
+  static constexpr int kV = kK + kStagesK * kKBytes;
+  static constexpr int kRaw = kV + kStagesV * kVBytes;
+  static constexpr int kMeta = kRaw + kRaws * kRawBytes;  // [8 tiles][8 groups of 16 keys] page_scales
   static constexpr int kBar = kMeta + (FP8 ? 8 * 8 * 16 : 0);
-  // q_full[2], k_full[S], v_full[S], k_empty[S], v_empty[S], v_land[S], s_full[2], p_full[2], o_full[2], drain,
-  // kraw_full[2], kraw_empty[2], vraw_full[2], vraw_empty[2], seg_full[kSegs], seg_empty[kSegs]
+  // q_full[2], k_full[], v_full[], k_empty[], v_empty[], v_land[], s_full[2], p_full[2], o_full[2], drain, raw_empty[],
+  // seg_full[kSegs], seg_empty[kSegs]
   static constexpr int kSegs = 4;
-  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 8 + 2 * kSegs;
+  static constexpr int kNumBars = 2 + 2 * kStagesK + 3 * kStagesV + 6 + 1 + kRaws + 2 * kSegs;
   static constexpr int kSeg = kBar + kNumBars * 8 + (kNumBars & 1) * 8;
   static constexpr int kMisc = kSeg + kSegs * 48;
   static constexpr int kBytes = kMisc + 16 + 16 * 8;
@@ -75,6 +79,24 @@ struct PrefillLayout {
 // Halves: the instruction descriptor of bf16 without its two type bits.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
   return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// e4m3 operands (kind::f8f6f4, both of type 0), fp32 accumulate; 32 of K an instruction.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, "
+      "p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// K-major rows of 64 bytes under the 64-byte swizzle (8-row groups of 512 bytes).
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(4) << 61);
 }
 
 // ------------------------------------------------------------------------------------- the plan
@@ -279,8 +301,7 @@ __global__ void __launch_bounds__(384, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const PrefillParams prm) {
   using L = PrefillLayout<D, FP8>;
-  constexpr int S = L::kStages;
-  constexpr int T = L::kTileBytes;
+  constexpr int SK = L::kStagesK, SV = L::kStagesV, TK = L::kKBytes, TV = L::kVBytes;
   extern __shared__ __align__(1024) uint8_t smem[];
   grid_dependency_launch();
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled tiles need a 1024-byte aligned base
@@ -290,19 +311,16 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* q_full = bars;
   uint64_t* k_full = bars + 2;
-  uint64_t* v_full = k_full + S;
-  uint64_t* k_empty = v_full + S;
-  uint64_t* v_empty = k_empty + S;
-  uint64_t* v_land = v_empty + S;  // bf16: V's copies have landed (v_full: and what is behind the end is zero)
-  uint64_t* s_full = v_land + S;
+  uint64_t* k_empty = k_full + SK;
+  uint64_t* v_full = k_empty + SK;  // V's tile is ready: halves of e4m3 codes, or zeros behind the end
+  uint64_t* v_empty = v_full + SV;
+  uint64_t* v_land = v_empty + SV;  // V's copies have landed (e4m3: in the staging ring, kRaws of them)
+  uint64_t* s_full = v_land + SV;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* drain = o_full + 2;
-  uint64_t* kraw_full = drain + 1;
-  uint64_t* kraw_empty = kraw_full + 2;
-  uint64_t* vraw_full = kraw_empty + 2;
-  uint64_t* vraw_empty = vraw_full + 2;
-  uint64_t* seg_full = vraw_empty + 2;
+  uint64_t* raw_empty = drain + 1;
+  uint64_t* seg_full = raw_empty + L::kRaws;
   uint64_t* seg_empty = seg_full + L::kSegs;
   PrefillSegment* segs = reinterpret_cast<PrefillSegment*>(smem + L::kSeg);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
@@ -313,13 +331,16 @@ __global__ void __launch_bounds__(384, 1)
   const PrefillShare share = prefill_share<384>(prm, blockIdx.x, scratch);
   if (share.b >= prm.b.B) return;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < SK; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&v_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(&v_full[s], FP8 ? 2 : 1);  // both converting warps, or the one that zeroes
       mbar_init(&v_empty[s], 1);
       mbar_init(&v_land[s], 1);
     }
+    for (int i = 0; i < L::kRaws; ++i) mbar_init(&raw_empty[i], 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 128);
       mbar_init(&s_full[t], 1);
@@ -327,8 +348,6 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&o_full[t], 1);
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < 2; ++i)
-      for (uint64_t* b : {kraw_full, kraw_empty, vraw_full, vraw_empty}) mbar_init(b + i, 1);
     for (int i = 0; i < L::kSegs; ++i) {
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 11);  // the MMA thread, warps 2 and 3, eight softmax warps
@@ -370,11 +389,10 @@ __global__ void __launch_bounds__(384, 1)
       prefetch_tmap(&tmV);
       PrefillWalk w;
       w.start(prm, share, blockIdx.x);
-      const int shift = min(prm.b.page_shift, FP8 ? 6 : 7), box_rows = 1 << shift;  // e4m3 lands in halves of 64 keys
+      const int shift = min(prm.b.page_shift, 7), box_rows = 1 << shift;
       constexpr int kCols = FP8 ? D : 64;
       bool ok = true, more = true;
-      int kt = 0;                      // key tiles since the start
-      int kn[2] = {0, 0}, vn[2] = {0, 0};  // loads issued (e4m3: of each half; bf16: [0])
+      int kt = 0, kn = 0, vn = 0;  // key tiles since the start, loads issued
       while (ok) {
         const int si = seg_n % L::kSegs;
         if (!(ok = wait_warp(&seg_empty[si], ((seg_n / L::kSegs) & 1) ^ 1, g, kSitePrefill | 16))) break;
@@ -407,84 +425,69 @@ __global__ void __launch_bounds__(384, 1)
             y = key & ((1 << prm.b.page_shift) - 1);
             if (FP8 && page >= 0) sc = page_scales(prm.Ks[z], prm.Vs[z]);
           }
-          if constexpr (FP8) {
-            // two halves of 64 keys each, K's then V's: a half's slot is free once its codes are halves
-            const int per_half = 64 >> shift;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int n = min(boxes - hf * per_half, per_half);
-              if (n <= 0) break;
-              const bool mine = lane >= hf * per_half && lane < hf * per_half + n;
-              const int bytes = n * box_rows * D, at = lane * box_rows * D;
-              if (!(ok = wait_warp(&kraw_empty[hf], (kn[hf] & 1) ^ 1, g, kSitePrefill | 1))) break;
-              ++kn[hf];
-              if (mine) {
-                // the scales of the page's groups of 16 keys; of the eight slots the one written here was last
-                // read for tile kt - 8, and the S that the operand ring has already seen done come after that
-                float4* m = reinterpret_cast<float4*>(smem + L::kMeta) + (kt & 7) * 8 + (lane << (shift - 4));
-                for (int i = 0; i < 1 << (shift - 4); ++i) m[i] = sc;
-              }
-              __syncwarp();
-              if (lane == 0) mbar_expect_tx(&kraw_full[hf], bytes);
-              __syncwarp();
-              if (mine) tma_load_3d(smem + L::kRawK + at, &tmK, 0, y, z, &kraw_full[hf]);
-              if (!(ok = wait_warp(&vraw_empty[hf], (vn[hf] & 1) ^ 1, g, kSitePrefill | 2))) break;
-              ++vn[hf];
-              if (lane == 0) mbar_expect_tx(&vraw_full[hf], bytes);
-              __syncwarp();
-              if (mine) tma_load_3d(smem + L::kRawV + at, &tmV, 0, y, z, &vraw_full[hf]);
-            }
-          } else {
-            const int s = kt % S, bytes = boxes * box_rows * D * 2;
-            const uint32_t ph = (kt / S) & 1;
-            if (!(ok = wait_warp(&k_empty[s], ph ^ 1, g, kSitePrefill | 1))) break;
-            if (lane == 0) mbar_expect_tx(&k_full[s], bytes);
-            __syncwarp();
-            if (lane < boxes)
-              for (int c = 0; c < D / kCols; ++c)
-                tma_load_3d(smem + L::kK + s * T + c * 16384 + lane * box_rows * 128, &tmK, c * kCols, y, z, &k_full[s]);
-            ++kn[0];
-            if (!(ok = wait_warp(&v_empty[s], ph ^ 1, g, kSitePrefill | 2))) break;
-            if (lane == 0) mbar_expect_tx(&v_land[s], bytes);
-            __syncwarp();
-            if (lane < boxes)
-              for (int c = 0; c < D / kCols; ++c)
-                tma_load_3d(smem + L::kV + s * T + c * 16384 + lane * box_rows * 128, &tmV, c * kCols, y, z, &v_land[s]);
-            ++vn[0];
+          constexpr int kSize = FP8 ? 1 : 2, VR = FP8 ? L::kRaws : SV;
+          const int sk = kt % SK, sv = kt % VR, bytes = boxes * box_rows * D * kSize;
+          if (!(ok = wait_warp(&k_empty[sk], ((kt / SK) & 1) ^ 1, g, kSitePrefill | 1))) break;
+          if (FP8 && lane < boxes) {
+            // the scales of the page's groups of 16 keys; of the eight slots the one written here was last
+            // read for tile kt - 8, and the S of tile kt - SK that freed the stage came after that
+            float4* m = reinterpret_cast<float4*>(smem + L::kMeta) + (kt & 7) * 8 + (lane << (shift - 4));
+            for (int i = 0; i < 1 << (shift - 4); ++i) m[i] = sc;
           }
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(&k_full[sk], bytes);
+          __syncwarp();
+          const int at = lane * box_rows * kCols * kSize;
+          if (lane < boxes)
+            for (int c = 0; c < D / kCols; ++c)
+              tma_load_3d(smem + L::kK + sk * TK + c * 16384 + at, &tmK, c * kCols, y, z, &k_full[sk]);
+          ++kn;
+          if (!(ok = wait_warp(FP8 ? &raw_empty[sv] : &v_empty[sv], ((kt / VR) & 1) ^ 1, g, kSitePrefill | 2))) break;
+          if (lane == 0) mbar_expect_tx(&v_land[sv], bytes);
+          __syncwarp();
+          if (lane < boxes)
+            for (int c = 0; c < D / kCols; ++c)
+              tma_load_3d(smem + (FP8 ? L::kRaw + sv * L::kRawBytes : L::kV + sv * TV) + c * 16384 + at, &tmV, c * kCols,
+                          y, z, &v_land[sv]);
+          ++vn;
         }
         if (ok) more = w.next(prm);
       }
       if (!ok) {  // let copies already in flight land before the CTA exits
-        if constexpr (FP8) {
-          for (int hf = 0; hf < 2; ++hf) {
-            if (kn[hf] > 0) drain_wait(&kraw_full[hf], (kn[hf] - 1) & 1);
-            if (vn[hf] > 0) drain_wait(&vraw_full[hf], (vn[hf] - 1) & 1);
-          }
-        } else {
-          for (int i = max(kn[0] - S, 0); i < kn[0]; ++i) drain_wait(&k_full[i % S], (i / S) & 1);
-          for (int i = max(vn[0] - S, 0); i < vn[0]; ++i) drain_wait(&v_land[i % S], (i / S) & 1);
-        }
+        constexpr int VR = FP8 ? L::kRaws : SV;
+        for (int i = max(kn - SK, 0); i < kn; ++i) drain_wait(&k_full[i % SK], (i / SK) & 1);
+        for (int i = max(vn - VR, 0); i < vn; ++i) drain_wait(&v_land[i % VR], (i / VR) & 1);
       }
     } else if (warp == 1) {
       // --------------------------------------------------------------------------------- MMA
       // One thread issues every UMMA, in the order of the contiguous forward.
       if (lane == 0) {
-        constexpr uint32_t idS = FP8 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t idO = FP8 ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
         const uint32_t sQ = smem_u32(smem + L::kQ), sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV);
         auto issue_s = [&](int t, int s) {
+          if constexpr (FP8) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_ss(tmem + 128 * t, sdesc_sw128(sQ + t * T + off, 16, 1024), sdesc_sw128(sK + s * T + off, 16, 1024),
-                   idS, kk > 0);
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk) {
+                const uint32_t a = sQ + t * L::kQBytes + part * (kTile * D) + kk * 32, b = sK + s * TK + kk * 32;
+                mma_ss_e4m3(tmem + 128 * t, D == 128 ? sdesc_sw128(a, 16, 1024) : sdesc_sw64(a),
+                            D == 128 ? sdesc_sw128(b, 16, 1024) : sdesc_sw64(b), idS, part + kk > 0);
+              }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              mma_ss(tmem + 128 * t, sdesc_sw128(sQ + t * L::kQBytes + off, 16, 1024),
+                     sdesc_sw128(sK + s * TK + off, 16, 1024), idS, kk > 0);
+            }
           }
         };
         auto issue_pv = [&](int t, int s, bool acc) {
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, sdesc_sw128(sV + s * T + kk * 2048, 16384, 1024), idO,
+            mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, sdesc_sw128(sV + s * TV + kk * 2048, 16384, 1024), idO,
                    (acc || kk > 0) ? 1u : 0u);
         };
         bool ok = true;
@@ -495,19 +498,19 @@ __global__ void __launch_bounds__(384, 1)
           const int last = max(end[0], end[1]);
           segment_done(true);
           if (last == t0) continue;
-          if (!(ok = wait(&k_full[kt % S], (kt / S) & 1, g, kSitePrefill | 3))) break;
+          if (!(ok = wait(&k_full[kt % SK], (kt / SK) & 1, g, kSitePrefill | 3))) break;
           for (int t = 0; t < 2 && ok; ++t)
             if (end[t] > t0) {
               if (!(ok = wait(&q_full[t], qn[t]++ & 1, g, kSitePrefill | 4))) break;
               tc_fence_after();
-              issue_s(t, kt % S);
+              issue_s(t, kt % SK);
               tc_commit(&s_full[t]);
             }
           if (!ok) break;
-          tc_commit(&k_empty[kt % S]);
+          tc_commit(&k_empty[kt % SK]);
           for (int j = t0; ok && j < last; ++j, ++kt) {
-            const int s = kt % S, s1 = (kt + 1) % S;
-            if (!(ok = wait(&v_full[s], (kt / S) & 1, g, kSitePrefill | 5))) break;
+            const int s = kt % SV, s1 = (kt + 1) % SK;
+            if (!(ok = wait(&v_full[s], (kt / SV) & 1, g, kSitePrefill | 5))) break;
             for (int t = 0; t < 2 && ok; ++t) {
               if (j >= end[t]) continue;
               if (!(ok = wait(&p_full[t], steps[t]++ & 1, g, kSitePrefill | 7))) break;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(384, 1)
               issue_pv(t, s, j > t0);
               tc_commit(&o_full[t]);
               if (j + 1 < end[t]) {
-                if (!(ok = wait(&k_full[s1], ((kt + 1) / S) & 1, g, kSitePrefill | 8))) break;
+                if (!(ok = wait(&k_full[s1], ((kt + 1) / SK) & 1, g, kSitePrefill | 8))) break;
                 tc_fence_after();
                 issue_s(t, s1);
                 tc_commit(&s_full[t]);
@@ -532,58 +535,50 @@ __global__ void __launch_bounds__(384, 1)
         drain_wait(drain, 0);
       }
     } else if constexpr (FP8) {
-      // ----------------------------------------------- e4m3 to halves: warp 2 K, warp 3 V
-      const bool is_v = warp == 3;
-      uint64_t *rfull = is_v ? vraw_full : kraw_full, *rempty = is_v ? vraw_empty : kraw_empty;
-      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-      const uint32_t raw = smem_u32(smem + (is_v ? L::kRawV : L::kRawK));
+      // -------------------- V's codes to halves: warp 2 the first 64 keys of a tile, warp 3 the others
+      const int first = (warp - 2) * 64;
       bool ok = true;
-      int kt = 0, rn[2] = {0, 0};
+      int kt = 0;
       while (const PrefillSegment* w = segment(ok, kWarp)) {
         const int t0 = w->t0, end = max(w->end[0], w->end[1]), len = w->len;
         __syncwarp();
         segment_done(lane == 0);
         for (int j = t0; j < end && ok; ++j, ++kt) {
-          const int s = kt % S;
+          const int s = kt % SV, rs = kt % L::kRaws;
+          if (!(ok = wait_warp(&v_land[rs], (kt / L::kRaws) & 1, g, kSitePrefill | 9))) break;
+          if (!(ok = wait_warp(&v_empty[s], ((kt / SV) & 1) ^ 1, g, kSitePrefill | 10))) break;
           const int live = len - j * kTile;  // rows behind it become zeros
-          const uint32_t to = smem_u32(smem + (is_v ? L::kV : L::kK) + s * T);
+          const uint32_t raw = smem_u32(smem + L::kRaw + rs * L::kRawBytes), to = smem_u32(smem + L::kV + s * TV);
           constexpr int CH = D / 16;  // 16-byte chunks of a row of codes
-#pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            const bool loaded = hf == 0 || live > 64;
-            if (loaded && !(ok = wait_warp(&rfull[hf], rn[hf]++ & 1, g, kSitePrefill | 9))) break;
-            if (hf == 0 && !(ok = wait_warp(&empty[s], ((kt / S) & 1) ^ 1, g, kSitePrefill | 10))) break;
-            // eight lanes store rows r and r + 1 (of 4 chunks each): no two to the same bank
+          // eight lanes store rows r and r + 1 (of 4 chunks each): no two to the same bank
 #pragma unroll 4
-            for (int i = 0; i < 64 * CH / 32; ++i) {
-              int r, c;
-              if constexpr (D == 128) {
-                r = hf * 64 + (i >> 1) * 8 + (lane >> 2), c = (lane & 3) + 4 * (i & 1);
-              } else {
-                r = hf * 64 + i * 8 + (lane >> 2), c = lane & 3;
-              }
-              const uint32_t from = D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4) : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-              uint4 x = lds128(from);
-              if (r >= live) x = make_uint4(0u, 0u, 0u, 0u);
-              uint32_t h[8];
-              halves_of_e4m3(x.x, h[0], h[1]);
-              halves_of_e4m3(x.y, h[2], h[3]);
-              halves_of_e4m3(x.z, h[4], h[5]);
-              halves_of_e4m3(x.w, h[6], h[7]);
-              const uint32_t at = to + (c >> 2) * 16384 + r * 128, c2 = 2 * (c & 3);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2) ^ (r & 7)) << 4)), "r"(h[0]),
-                           "r"(h[1]), "r"(h[2]), "r"(h[3])
-                           : "memory");
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2 + 1) ^ (r & 7)) << 4)), "r"(h[4]),
-                           "r"(h[5]), "r"(h[6]), "r"(h[7])
-                           : "memory");
+          for (int i = 0; i < 64 * CH / 32; ++i) {
+            int r, c;
+            if constexpr (D == 128) {
+              r = first + (i >> 1) * 8 + (lane >> 2), c = (lane & 3) + 4 * (i & 1);
+            } else {
+              r = first + i * 8 + (lane >> 2), c = lane & 3;
             }
-            if (hf == 1) fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              if (loaded) mbar_arrive(&rempty[hf]);
-              if (hf == 1) mbar_arrive(&full[s]);
-            }
+            uint4 x = lds128(D == 128 ? raw + r * 128 + ((c ^ (r & 7)) << 4) : raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+            if (r >= live) x = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t h[8];
+            halves_of_e4m3(x.x, h[0], h[1]);
+            halves_of_e4m3(x.y, h[2], h[3]);
+            halves_of_e4m3(x.z, h[4], h[5]);
+            halves_of_e4m3(x.w, h[6], h[7]);
+            const uint32_t at = to + (c >> 2) * 16384 + r * 128, c2 = 2 * (c & 3);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2) ^ (r & 7)) << 4)), "r"(h[0]),
+                         "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c2 + 1) ^ (r & 7)) << 4)), "r"(h[4]),
+                         "r"(h[5]), "r"(h[6]), "r"(h[7])
+                         : "memory");
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_full[s]);
+            mbar_arrive(&raw_empty[rs]);
           }
         }
         if (!ok) break;
@@ -597,13 +592,13 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         segment_done(lane == 0);
         for (int j = t0; j < end && ok; ++j, ++kt) {
-          const int live = len - j * kTile, s = kt % S;
-          if (!(ok = wait_warp(&v_land[s], (kt / S) & 1, g, kSitePrefill | 11))) break;
+          const int live = len - j * kTile, s = kt % SV;
+          if (!(ok = wait_warp(&v_land[s], (kt / SV) & 1, g, kSitePrefill | 11))) break;
           if (live < kTile) {
             for (int i = lane; i < (kTile - live) * 8; i += 32)
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                *reinterpret_cast<uint4*>(smem + L::kV + s * T + c * 16384 + live * 128 + i * 16) =
+                *reinterpret_cast<uint4*>(smem + L::kV + s * TV + c * 16384 + live * 128 + i * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async();
             __syncwarp();
@@ -652,22 +647,38 @@ __global__ void __launch_bounds__(384, 1)
             for (int k = 0; k < 4; ++k)
               amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
           }
-          // a power of two above the row's largest magnitude (kept where its inverse is normal)
-          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 2), 252);
-          sl2 *= __uint_as_float(static_cast<uint32_t>(e) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+          // q * 256 / (a power of two above the row's largest magnitude) = first part + second part, both e4m3
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 252);
+          sl2 *= __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t part[2][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              v[k] = pack_half2(__uint_as_float(v[k] << 16) * down, __uint_as_float(v[k] & 0xFFFF0000u) * down);
-            x[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int k = 0; k < 4; ++k) {
+              const uint4& y = x[2 * i + (k >> 1)];
+              const uint32_t v0 = k & 1 ? y.z : y.x, v1 = k & 1 ? y.w : y.y;
+              const float f[4] = {__uint_as_float(v0 << 16) * down, __uint_as_float(v0 & 0xFFFF0000u) * down,
+                                  __uint_as_float(v1 << 16) * down, __uint_as_float(v1 & 0xFFFF0000u) * down};
+              part[0][k] = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+              uint32_t h0, h1;
+              halves_of_e4m3(part[0][k], h0, h1);
+              const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+              const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+              part[1][k] = e4m3x2(f[0] - a.x, f[1] - a.y) | (e4m3x2(f[2] - b.x, f[3] - b.y) << 16);
+            }
+            const int at = D == 128 ? r * 128 + ((i ^ (r & 7)) << 4) : r * 64 + ((i ^ ((r >> 1) & 3)) << 4);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kQBytes + n * (kTile * D) + at) =
+                  make_uint4(part[n][0], part[n][1], part[n][2], part[n][3]);
           }
-        }
+        } else {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4*>(smem + L::kQ + t * T + (i >> 3) * 16384 + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = x[i];
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kQBytes + (i >> 3) * 16384 + r * 128 +
+                                      (((i & 7) ^ (r & 7)) << 4)) = x[i];
+        }
         fence_proxy_async();
         mbar_arrive(&q_full[t]);
       }
