@@ -34,6 +34,13 @@ constexpr int kPreCtas = 148;
 constexpr int kPreRows = 256;     // query rows of an item: two tiles
 constexpr int kPreMinTiles = 2;   // a CTA's share is at least this many key tiles
 
+// Register split (setmaxnreg), the launch's total.  The issuing thread keeps its loop state and the
+// descriptors that the compiler holds: at the contiguous forward's 56 it spilled 28 words and reloaded them
+// between UMMAs (a 2048-token chunk over 16384 bf16 keys: 554 us against 493 us); the softmax fits 208.
+constexpr int kPreRegsCtl = 88, kPreRegsSoftmax = 208;
+static_assert(128 * kPreRegsCtl + 256 * kPreRegsSoftmax <= 384 * ((65536 / 384) / 8 * 8),
+              "prefill register split exceeds the launch's");
+
 struct PrefillParams {
   PagedBatch b;
   const __nv_bfloat16* Q;  // [T, Hq, D], ldq elements between tokens
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(384, 1)
   };
 
   if (warp < 4) {
-    regs_to<kFwdRegsCtl, L::kLaunchRegs>();
+    regs_to<kPreRegsCtl, L::kLaunchRegs>();
     if (warp == 0) {
       // ---------------------------------------------------------------------------- producer
       // Lane i issues the boxes of a tile's i-th page.
@@ -428,9 +435,10 @@ __global__ void __launch_bounds__(384, 1)
           constexpr int kSize = FP8 ? 1 : 2, VR = FP8 ? L::kRaws : SV;
           const int sk = kt % SK, sv = kt % VR, bytes = boxes * box_rows * D * kSize;
           if (!(ok = wait_warp(&k_empty[sk], ((kt / SK) & 1) ^ 1, g, kSitePrefill | 1))) break;
-          if (FP8 && lane < boxes) {
-            // the scales of the page's groups of 16 keys; of the eight slots the one written here was last
-            // read for tile kt - 8, and the S of tile kt - SK that freed the stage came after that
+          if (FP8 && lane < (kTile >> shift)) {
+            // the scales of the page's groups of 16 keys (neutral ones behind the last page); of the eight slots
+            // the one written here was last read for tile kt - 8, and the S of tile kt - SK that freed the stage
+            // came after that
             float4* m = reinterpret_cast<float4*>(smem + L::kMeta) + (kt & 7) * 8 + (lane << (shift - 4));
             for (int i = 0; i < 1 << (shift - 4); ++i) m[i] = sc;
           }
@@ -490,44 +498,50 @@ __global__ void __launch_bounds__(384, 1)
             mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * kk, sdesc_sw128(sV + s * TV + kk * 2048, 16384, 1024), idO,
                    (acc || kk > 0) ? 1u : 0u);
         };
+        // Per-tile state is kept in bits and selected, not indexed: an indexed array would live in local memory,
+        // and every load of it would delay the thread that feeds the tensor core.
         bool ok = true;
         int kt = 0;
-        int qn[2] = {0, 0}, steps[2] = {0, 0};  // query tiles loaded, tile steps done
+        uint32_t q_ph = 0, p_ph = 0;  // bit t: parity of the tile's next q_full, p_full
         while (const PrefillSegment* w = segment(ok, kThread)) {
-          const int t0 = w->t0, end[2] = {w->end[0], w->end[1]};
-          const int last = max(end[0], end[1]);
+          const int t0 = w->t0, end0 = w->end[0], end1 = w->end[1];
+          const int last = max(end0, end1);
           segment_done(true);
           if (last == t0) continue;
           if (!(ok = wait(&k_full[kt % SK], (kt / SK) & 1, g, kSitePrefill | 3))) break;
-          for (int t = 0; t < 2 && ok; ++t)
-            if (end[t] > t0) {
-              if (!(ok = wait(&q_full[t], qn[t]++ & 1, g, kSitePrefill | 4))) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (ok && (t ? end1 : end0) > t0) {
+              if (!(ok = wait(&q_full[t], (q_ph >> t) & 1, g, kSitePrefill | 4))) break;
+              q_ph ^= 1u << t;
               tc_fence_after();
               issue_s(t, kt % SK);
               tc_commit(&s_full[t]);
             }
           if (!ok) break;
           tc_commit(&k_empty[kt % SK]);
-          for (int j = t0; ok && j < last; ++j, ++kt) {
+          for (int j = t0; j < last; ++j, ++kt) {
             const int s = kt % SV, s1 = (kt + 1) % SK;
             if (!(ok = wait(&v_full[s], (kt / SV) & 1, g, kSitePrefill | 5))) break;
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (j >= end[t]) continue;
-              if (!(ok = wait(&p_full[t], steps[t]++ & 1, g, kSitePrefill | 7))) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int end = t ? end1 : end0;
+              if (!ok || j >= end) continue;
+              if (!(ok = wait(&p_full[t], (p_ph >> t) & 1, g, kSitePrefill | 7))) continue;
+              p_ph ^= 1u << t;
               tc_fence_after();
               issue_pv(t, s, j > t0);
               tc_commit(&o_full[t]);
-              if (j + 1 < end[t]) {
-                if (!(ok = wait(&k_full[s1], ((kt + 1) / SK) & 1, g, kSitePrefill | 8))) break;
+              if (j + 1 < end) {
+                if (!(ok = wait(&k_full[s1], ((kt + 1) / SK) & 1, g, kSitePrefill | 8))) continue;
                 tc_fence_after();
                 issue_s(t, s1);
                 tc_commit(&s_full[t]);
               }
             }
-            if (ok) {
-              tc_commit(&v_empty[s]);
-              if (j + 1 < last) tc_commit(&k_empty[s1]);
-            }
+            if (!ok) break;
+            tc_commit(&v_empty[s]);
+            if (j + 1 < last) tc_commit(&k_empty[s1]);
           }
           if (!ok) break;
         }
@@ -613,7 +627,7 @@ __global__ void __launch_bounds__(384, 1)
       while (segment(ok, kThread)) segment_done(true);
     }
   } else {
-    regs_to<kFwdRegsSoftmax, L::kLaunchRegs>();
+    regs_to<kPreRegsSoftmax, L::kLaunchRegs>();
     // ------------------------------------------- Q, softmax / correction / epilogue: a thread a row
     const int t = (warp - 4) >> 2;   // query tile
     const int quarter = warp & 3;    // TMEM lanes this warp may touch
@@ -701,6 +715,8 @@ __global__ void __launch_bounds__(384, 1)
         const float4* mt = meta + ((kt0 + j - t0) & 7) * 8;
         // row maximum (e4m3: of each group of 16 keys, then with the group's scales)
         float top;
+        float fg[FP8 ? 8 : 1];  // e4m3: each group's score factor
+        bool tiny = false;      // e4m3: a group's value scale needs the boost (page_scales)
         if constexpr (FP8) {
           float mg[8];
 #pragma unroll
@@ -711,11 +727,10 @@ __global__ void __launch_bounds__(384, 1)
             m0 = fmax3(m0, S(16 * q + 10), S(16 * q + 11));
             m1 = fmax3(m1, S(16 * q + 12), S(16 * q + 13));
             m0 = fmax3(m0, S(16 * q + 14), S(16 * q + 15));
-            const bool live = j * kTile + 16 * q < len;  // a page behind the end brought no scales
             const float4 sc = mt[q];
-            // a group that is wholly masked stays at -inf whatever its scale (zero too)
-            const float x = fmaxf(m0, m1);
-            mg[q] = live && x > -INFINITY ? fmaf(x, sl2 * sc.x, sc.y) : -INFINITY;
+            fg[q] = fmaxf(sl2 * sc.x, 1e-37f);  // not zero, which a masked score would turn into NaN
+            mg[q] = fmaf(fmaxf(m0, m1), fg[q], sc.y);
+            tiny |= sc.w > 0.0f;
           }
           top = fmaxf(fmax3(mg[0], mg[1], mg[2]), fmax3(mg[3], mg[4], fmax3(mg[5], mg[6], mg[7])));
         } else {
@@ -739,45 +754,45 @@ __global__ void __launch_bounds__(384, 1)
         const float m_sub = m_ref == -INFINITY ? 0.0f : m_ref;
         float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
         // P, 32 keys -> 16 columns at a time, over S
+        auto exp_store = [&](auto tiny_tag) {
+          constexpr bool kTiny = decltype(tiny_tag)::value;
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t pk[16];
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float2 c2 = make_float2(sl2, sl2), nm2 = make_float2(-m_sub, -m_sub);
-            float inv = 1.0f;
-            bool tiny = false;
-            if constexpr (FP8) {
-              const bool live = j * kTile + 32 * cc + 16 * hh < len;
-              const float4 sc = mt[2 * cc + hh];
-              const float f = live ? fmaxf(sl2 * sc.x, 1e-37f) : 1.0f, n = live ? sc.y + sc.w - m_sub : 0.0f;
-              inv = live ? sc.z : 0.0f;
-              tiny = live && sc.w > 0.0f;
-              c2 = make_float2(f, f);
-              nm2 = make_float2(n, n);
-            }
-            float2 gs = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int c = 32 * cc + 16 * hh + 2 * e;
-              const float2 x = __ffma2_rn(make_float2(S(c), S(c + 1)), c2, nm2);
-              float2 p;
-              p.x = exp2_sfu(x.x);
-              p.y = exp2_sfu(x.y);
+            for (int hh = 0; hh < 2; ++hh) {
+              float2 c2 = make_float2(sl2, sl2), nm2 = make_float2(-m_sub, -m_sub), gs = make_float2(0.f, 0.f);
+              float4 sc = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
               if constexpr (FP8) {
-                gs = __fadd2_rn(gs, p);
-                if (tiny) p.x *= kUnboost, p.y *= kUnboost;
-                pk[8 * hh + e] = pack_half2(p.x, p.y);
-              } else {
-                if (e & 1) ls1 = __fadd2_rn(ls1, p);
-                else ls0 = __fadd2_rn(ls0, p);
-                pk[8 * hh + e] = pack_bf16x2(p.x, p.y);
+                sc = mt[2 * cc + hh];
+                const float n = (kTiny ? sc.y + sc.w : sc.y) - m_sub;
+                c2 = make_float2(fg[2 * cc + hh], fg[2 * cc + hh]);
+                nm2 = make_float2(n, n);
               }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int c = 32 * cc + 16 * hh + 2 * e;
+                const float2 x = __ffma2_rn(make_float2(S(c), S(c + 1)), c2, nm2);
+                float2 p;
+                p.x = exp2_sfu(x.x);
+                p.y = exp2_sfu(x.y);
+                if constexpr (FP8) {
+                  gs = __fadd2_rn(gs, p);
+                  if (kTiny && sc.w > 0.0f) p.x *= kUnboost, p.y *= kUnboost;
+                  pk[8 * hh + e] = pack_half2(p.x, p.y);
+                } else {
+                  if (e & 1) ls1 = __fadd2_rn(ls1, p);
+                  else ls0 = __fadd2_rn(ls0, p);
+                  pk[8 * hh + e] = pack_bf16x2(p.x, p.y);
+                }
+              }
+              if constexpr (FP8) ls0 = __ffma2_rn(gs, make_float2(sc.z, sc.z), ls0);
             }
-            if constexpr (FP8) ls0 = __ffma2_rn(gs, make_float2(inv, inv), ls0);
+            tmem_st16(tS + 16 * cc, pk);
           }
-          tmem_st16(tS + 16 * cc, pk);
-        }
+        };
+        if (FP8 && tiny) exp_store(std::true_type{});
+        else exp_store(std::false_type{});
 #undef S
         const float2 ls = __fadd2_rn(ls0, ls1);
         l += ls.x + ls.y;
