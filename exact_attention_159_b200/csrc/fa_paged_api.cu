@@ -129,16 +129,26 @@ int launch_append(const fa::AppendParams& prm, long long grid, int most, cudaStr
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct PagedWs {
-  size_t dec_o, dec_ml, pre_o, pre_ml, total;
+  size_t dec_plan, dec_o, dec_ml, pre_plan, pre_o, pre_ml, total;
 };
 // The kernel of many rows has its parts only where a sequence may have as many.
 PagedWs paged_ws(int d, bool many) {
   PagedWs w;
-  w.dec_o = 0;
-  w.dec_ml = round256(static_cast<size_t>(2) * fa::kDecCtas * fa::kDecRows * d * 4);
-  w.pre_o = w.dec_ml + round256(static_cast<size_t>(2) * fa::kDecCtas * fa::kDecRows * 8);
-  w.pre_ml = w.pre_o + (many ? round256(static_cast<size_t>(2) * fa::kPreCtas * fa::kPreRows * d * 4) : 0);
-  w.total = w.pre_ml + (many ? round256(static_cast<size_t>(2) * fa::kPreCtas * fa::kPreRows * 8) : 0);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  const size_t dec = static_cast<size_t>(2) * fa::kDecCtas * fa::kDecRows;
+  const size_t pre = many ? static_cast<size_t>(2) * fa::kPreCtas * fa::kPreRows : 0;
+  w.dec_plan = take(fa::kDecCtas * sizeof(fa::CutPlan));
+  w.dec_o = take(dec * d * 4);
+  w.dec_ml = take(dec * 8);
+  w.pre_plan = take(fa::kPreCtas * sizeof(fa::CutPlan));
+  w.pre_o = take(pre * d * 4);
+  w.pre_ml = take(pre * 8);
+  w.total = at;
   return w;
 }
 bool many_rows(const fa_paged_batch* b, int T, int G) {
@@ -188,8 +198,8 @@ int launch_fwd_paged(const FwdMaps& m, const fa::DecodeParams& dec, const fa::Pr
   }
   const int dec_cuts = dec.whole ? 0 : fa::kDecCtas - 1, pre_cuts = many ? fa::kPreCtas - 1 : 0;
   if (dec_cuts + pre_cuts == 0) return FA_OK;
-  return launch_overlapped(fa::join_kernel<D>, dec_cuts + pre_cuts * fa::kJoinSplit, fa::kJoinThreads, 0, st, dec, pre,
-                           dec_cuts + 1)
+  return launch_overlapped(fa::join_kernel<D>, dec_cuts * dec.rows + pre_cuts * fa::kJoinPreSplit, fa::kJoinThreads, 0,
+                           st, dec, pre, dec_cuts + 1)
              ? FA_OK
              : FA_ERR_CUDA;
 }
@@ -325,6 +335,7 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   dec.LSE = LSE;
   dec.Ks = cache->K_scale;
   dec.Vs = cache->V_scale;
+  dec.plan = reinterpret_cast<fa::CutPlan*>(wsb + ws.dec_plan);
   dec.part_o = reinterpret_cast<float*>(wsb + ws.dec_o);
   dec.part_ml = reinterpret_cast<float2*>(wsb + ws.dec_ml);
   dec.G = G;
@@ -344,6 +355,7 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   pre.LSE = LSE;
   pre.Ks = dec.Ks;
   pre.Vs = dec.Vs;
+  pre.plan = reinterpret_cast<fa::CutPlan*>(wsb + ws.pre_plan);
   pre.part_o = reinterpret_cast<float*>(wsb + ws.pre_o);
   pre.part_ml = reinterpret_cast<float2*>(wsb + ws.pre_ml);
   pre.G = G;

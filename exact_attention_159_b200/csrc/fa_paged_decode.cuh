@@ -56,6 +56,24 @@ __device__ __forceinline__ float4 page_scales(float ks, float vs) {
   return make_float4(ks, lv, (tiny ? kUnboost : 1.0f) / vs, tiny ? kBoost : 0.0f);
 }
 
+// What the join needs of the cut before share c, left in the workspace by CTA c, whose share begins with tile
+// `tile` of an item of n.
+struct alignas(16) CutPlan {
+  long long per;
+  int tile, n;     // tile 0 (or no share at all): nothing is divided here
+  int h;           // key/value head
+  int row0, rows;  // the item's first row among the sequence's rows * G, and its number of rows
+  int token0;      // the sequence's first token row
+};
+// The shares `first`..`last` that an item lies in; first < c - 1: an earlier cut divides it too.
+struct Cut {
+  int first, last;
+};
+FA_HD Cut cut_of(long long per, int c, int tile, int n) {
+  const long long begin = per * c - tile;
+  return Cut{static_cast<int>(begin / per), static_cast<int>((begin + n - 1) / per)};
+}
+
 struct DecodeParams {
   PagedBatch b;
   const __nv_bfloat16* Q;  // [T, Hq, D], ldq elements between tokens
@@ -65,6 +83,7 @@ struct DecodeParams {
   const float *Ks, *Vs;
   float* part_o;      // [2 * n_cta][rows][D] unnormalised sums
   float2* part_ml;    // [2 * n_cta][rows] (m in log2 units, l)
+  CutPlan* plan;      // [n_cta]
   int G, Hq;
   int tile, rows;     // keys of a tile (DecodeLayout::kTile), query rows of an item (8 * NT)
   int max_rows;       // sequences of more rows * G are another kernel's
@@ -168,20 +187,6 @@ __device__ __forceinline__ DecodeShare decode_share(const DecodeParams& p, int i
 // Where CTA `cta` leaves the part of an item that starts at tile t0 of it: its share has at most one part
 // whose item began in an earlier share and one whose item goes on in the next.
 FA_HD int decode_slot(int cta, int t0) { return 2 * cta + (t0 == 0 ? 1 : 0); }
-
-// The item that the cut before share c divides: `first`..`last` are the shares it lies in.  first < c - 1
-// when an earlier cut divides it too, last < c when the cut falls between two items.
-struct DecodeCut {
-  int item, first, last;
-};
-FA_HD DecodeCut decode_cut(long long per, int c, long long off, int tiles) {
-  DecodeCut r;
-  r.item = static_cast<int>(off / tiles);
-  const long long tile = off % tiles, begin = per * c - tile;
-  r.first = static_cast<int>(begin / per);
-  r.last = tile == 0 ? c - 1 : static_cast<int>((begin + tiles - 1) / per);
-  return r;
-}
 
 // Walks a CTA's share: one segment (an item's tiles [t0, t1)) after another.
 struct DecodeWalk {
@@ -347,12 +352,18 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   }
   const DecodeShare share = decode_share<kDecThreads>(prm, blockIdx.x, gridDim.x, scratch);  // has the barriers
   if (share.b >= prm.b.B) {
+    if (threadIdx.x == 0) prm.plan[blockIdx.x] = CutPlan{};
     grid_dependency_wait();
     return;
   }
   const Guard g{abort_flag, prm.b.status};
   DecodeWalk w;
   w.start(prm, share, blockIdx.x);
+  if (threadIdx.x == 0) {
+    const int row0 = w.item / prm.b.Hkv * prm.rows;
+    prm.plan[blockIdx.x] = CutPlan{share.per, w.t0, w.d.tiles, w.item % prm.b.Hkv, row0,
+                                   min(prm.rows, w.d.s.rows * prm.G - row0), w.d.s.row0};
+  }
   const int box_shift = min(prm.b.page_shift, FP8 ? 7 : 6), box_rows = 1 << box_shift;
   int it = 0;  // tiles since the start: stage it % S
 

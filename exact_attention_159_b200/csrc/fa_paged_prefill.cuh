@@ -50,6 +50,7 @@ struct PrefillParams {
   const float *Ks, *Vs;
   float* part_o;      // [2 * kPreCtas][kPreRows][D] unnormalised sums
   float2* part_ml;    // [2 * kPreCtas][kPreRows] (m in log2 units, l)
+  CutPlan* plan;      // [kPreCtas]
   int G, Hq;
   int min_rows;       // sequences of no more rows * G are the other kernel's
   int causal;
@@ -108,18 +109,18 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
 
 // ------------------------------------------------------------------------------------- the plan
 // Sum of floor((a i + b) / m) over i = 0 .. n - 1 (all non-negative, m > 0): Euclid's steps on the lattice points
-// under the line.
-FA_HD long long floor_sum(long long n, long long m, long long a, long long b) {
+// under the line.  Here n < 2^24, b < 2^31 and a, m are small, so the divisions are of 32 bits.
+FA_HD long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    sum += static_cast<long long>(n) * (n - 1) / 2 * (a / m) + static_cast<long long>(n) * (b / m);
     a %= m;
     b %= m;
-    const long long y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long x = m;
+    const uint32_t x = m;
     m = a;
     a = x;
   }
@@ -131,7 +132,7 @@ struct PrefillSeq {
   int pairs;       // 0: no rows, or too few for this kernel
   int tiles;       // key tiles of the whole sequence (1 when it has no key: its rows are written)
   int linear;      // pair p counts (x + 2 p) / G + 1 tiles, the last one all; otherwise every pair counts all
-  long long x;
+  int x;
   int G;
   // Tiles counted before pair p (p < pairs), and pair p's own; a pair's rows see no tile beyond its own.
   FA_HD long long before(int p) const {
@@ -152,7 +153,7 @@ FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   // pair p's last row (when the pair is full) is token (256 (p + 1) - 1) / G, which sees keys up to len - rows +
   // that; a tile has 128 keys, and 256 p is a multiple of 128, which leaves (x + 2 p) / G
   d.linear = p.causal && d.s.len >= d.s.rows;
-  d.x = d.linear ? (static_cast<long long>(d.s.len - d.s.rows) * p.G + 255) / 128 : 0;
+  d.x = d.linear ? static_cast<int>((static_cast<long long>(d.s.len - d.s.rows) * p.G + 255) / 128) : 0;
   return d;
 }
 FA_HD long long prefill_per(long long total) {
@@ -177,18 +178,6 @@ FA_HD PrefillAt prefill_at(const PrefillSeq& d, long long off) {
   a.p = lo;
   a.tile = static_cast<int>(r - d.before(lo));
   return a;
-}
-
-// The item that the cut before share c falls into: `first`..`last` are the shares it lies in (as DecodeCut).
-struct PrefillCut {
-  int first, last;
-};
-FA_HD PrefillCut prefill_cut(long long per, int c, const PrefillAt& a, int n) {
-  const long long begin = per * c - a.tile;
-  PrefillCut r;
-  r.first = static_cast<int>(begin / per);
-  r.last = a.tile == 0 ? c - 1 : static_cast<int>((begin + n - 1) / per);
-  return r;
 }
 
 struct PrefillShare {
@@ -336,7 +325,10 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const PrefillShare share = prefill_share<384>(prm, blockIdx.x, scratch);
-  if (share.b >= prm.b.B) return;
+  if (share.b >= prm.b.B) {
+    if (threadIdx.x == 0) prm.plan[blockIdx.x] = CutPlan{};
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < SK; ++s) {
       mbar_init(&k_full[s], 1);
@@ -396,6 +388,9 @@ __global__ void __launch_bounds__(384, 1)
       prefetch_tmap(&tmV);
       PrefillWalk w;
       w.start(prm, share, blockIdx.x);
+      if (lane == 0)
+        prm.plan[blockIdx.x] = CutPlan{share.per, w.t0, w.n, w.h, w.p * kPreRows,
+                                       min(kPreRows, w.d.s.rows * prm.G - w.p * kPreRows), w.d.s.row0};
       const int shift = min(prm.b.page_shift, 7), box_rows = 1 << shift;
       constexpr int kCols = FP8 ? D : 64;
       bool ok = true, more = true;

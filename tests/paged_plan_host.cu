@@ -124,9 +124,13 @@ static void shares(std::mt19937& rng, bool whole) {
   for (int c = 1; c < n_cta; ++c) {
     const DecodeShare s = locate(c);
     if (s.b >= B) continue;
-    const DecodeCut cut = decode_cut(per, c, s.off, decode_seq(p, s.b).tiles);
-    if (cut.last < c || cut.first != c - 1) continue;
-    auto it = parts.find({s.b, cut.item});
+    DecodeWalk w;
+    w.start(p, s, c);
+    if (w.t0 == 0) continue;
+    const Cut cut = cut_of(per, c, w.t0, w.d.tiles);
+    REQUIRE(cut.last >= c && cut.first < c);
+    if (cut.first != c - 1) continue;
+    auto it = parts.find({s.b, w.item});
     REQUIRE(it != parts.end());
     std::vector<int> want;
     for (int k = c - 1; k <= cut.last; ++k) want.push_back(decode_slot(k, k - (c - 1)));
@@ -230,11 +234,13 @@ static void many_rows(std::mt19937& rng) {
   for (int c = 1; c < kPreCtas; ++c) {
     const PrefillShare s = locate(c);
     if (s.b >= B) continue;
-    const PrefillSeq d = prefill_seq(p, s.b);
-    const PrefillAt a = prefill_at(d, s.off);
-    const PrefillCut cut = prefill_cut(per, c, a, d.count(a.p));
-    if (cut.last < c || cut.first != c - 1) continue;
-    auto it = parts.find({s.b, a.h, a.p});
+    PrefillWalk w;
+    w.start(p, s, c);
+    if (w.t0 == 0) continue;
+    const Cut cut = cut_of(per, c, w.t0, w.n);
+    REQUIRE(cut.last >= c && cut.first < c);
+    if (cut.first != c - 1) continue;
+    auto it = parts.find({s.b, w.h, w.p});
     REQUIRE(it != parts.end());
     std::vector<int> want;
     for (int k = c - 1; k <= cut.last; ++k) want.push_back(decode_slot(k, k - (c - 1)));
