@@ -10,7 +10,8 @@
 //
 // Rows: the R = rows * G (token, query head) pairs that read one key/value head, in blocks of 8 * NT.  One
 // (sequence, row block, key/value head) is an item of ceil(len / tile) tiles; the items' tiles laid end to
-// end are cut into equal runs, one per CTA, so a batch of ragged lengths loads every SM alike.  An item
+// end, each with a unit more for its start and end, are cut into equal runs, one per CTA, so a batch of ragged
+// lengths loads every SM alike.  An item
 // that a cut divides leaves its unnormalised sums in the workspace, at most two a CTA, for the join.
 //
 // Each of the four consumer warps takes a quarter of every tile's keys and keeps its own maximum, sum and
@@ -41,6 +42,7 @@ constexpr int kDecCtas = 2 * 148;  // two on each SM
 constexpr int kDecThreads = 160;   // four consumer warps, one producer warp
 constexpr int kDecStageBytes = 98304;
 constexpr int kDecMinTiles = 2;    // a CTA's share is at least this many tiles
+constexpr int kDecItemCost = 1;    // tiles' worth of time that starting and ending an item takes
 constexpr float kDecTau = 8.0f;    // log2 units
 constexpr float kScaleFloor = 7.8886090522101181e-31f;  // 2^-100: smaller value scales count as this
 constexpr float kBoost = 100.0f, kUnboost = kScaleFloor;
@@ -60,7 +62,7 @@ __device__ __forceinline__ float4 page_scales(float ks, float vs) {
 // `tile` of an item of n.
 struct alignas(16) CutPlan {
   long long per;
-  int tile, n;     // tile 0 (or no share at all): nothing is divided here
+  int tile, n;     // tile 0 (or no tile in the share at all): nothing is divided here
   int h;           // key/value head
   int row0, rows;  // the item's first row among the sequence's rows * G, and its number of rows
   int token0;      // the sequence's first token row
@@ -124,11 +126,11 @@ FA_HD DecodeSeq decode_seq(const DecodeParams& p, int b) {
   return d;
 }
 FA_HD long long decode_units(const DecodeParams& p, const DecodeSeq& d) {
-  return static_cast<long long>(d.items) * (p.whole ? 1 : d.tiles);
+  return static_cast<long long>(d.items) * (p.whole ? 1 : d.tiles + kDecItemCost);
 }
 FA_HD long long decode_per(const DecodeParams& p, long long total, int n_cta) {
   const long long per = (total + n_cta - 1) / n_cta;
-  return !p.whole && per < kDecMinTiles ? kDecMinTiles : per;
+  return !p.whole && per < kDecMinTiles + kDecItemCost ? kDecMinTiles + kDecItemCost : per;
 }
 
 struct DecodeShare {
@@ -190,40 +192,41 @@ FA_HD int decode_slot(int cta, int t0) { return 2 * cta + (t0 == 0 ? 1 : 0); }
 
 // Walks a CTA's share: one segment (an item's tiles [t0, t1)) after another.
 struct DecodeWalk {
-  long long left;
-  int b, item, t0, t1;
+  long long left;  // units
+  int b, item, u0, t0, t1;
   DecodeSeq d;
   bool whole;
-  FA_HD void start(const DecodeParams& p, const DecodeShare& s, int index) {
+  // False when the share holds no tile.
+  FA_HD bool start(const DecodeParams& p, const DecodeShare& s, int index) {
     left = min(s.per, s.total - s.per * index);
     b = s.b;
     d = decode_seq(p, b);
-    if (p.whole) {
-      item = static_cast<int>(s.off);
-      t0 = 0;
-    } else {
-      item = static_cast<int>(s.off / d.tiles);
-      t0 = static_cast<int>(s.off % d.tiles);
-    }
+    const int units = d.tiles + kDecItemCost;
+    item = static_cast<int>(p.whole ? s.off : s.off / units);
+    u0 = p.whole ? 0 : static_cast<int>(s.off % units);
     cut(p);
+    return t1 > 0 || next(p);
   }
   FA_HD void cut(const DecodeParams& p) {
-    t1 = p.whole ? d.tiles : static_cast<int>(min(static_cast<long long>(d.tiles), t0 + left));
+    t0 = max(0, u0 - kDecItemCost);
+    t1 = p.whole ? d.tiles : max(0, static_cast<int>(min(static_cast<long long>(d.tiles + kDecItemCost), u0 + left)) - kDecItemCost);
     whole = t0 == 0 && t1 == d.tiles;
   }
   // False when the share is done.
   FA_HD bool next(const DecodeParams& p) {
-    left -= p.whole ? 1 : t1 - t0;
-    if (left <= 0) return false;
-    t0 = 0;
-    if (++item == d.items) {
-      item = 0;
-      do {
-        if (++b >= p.b.B) return false;
-        d = decode_seq(p, b);
-      } while (d.items == 0);
-    }
-    cut(p);
+    do {
+      left -= p.whole ? 1 : d.tiles + kDecItemCost - u0;
+      if (left <= 0) return false;
+      u0 = 0;
+      if (++item == d.items) {
+        item = 0;
+        do {
+          if (++b >= p.b.B) return false;
+          d = decode_seq(p, b);
+        } while (d.items == 0);
+      }
+      cut(p);
+    } while (t1 == 0);
     return true;
   }
 };
@@ -351,14 +354,13 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     fence_mbar_init();
   }
   const DecodeShare share = decode_share<kDecThreads>(prm, blockIdx.x, gridDim.x, scratch);  // has the barriers
-  if (share.b >= prm.b.B) {
+  DecodeWalk w;
+  if (share.b >= prm.b.B || !w.start(prm, share, blockIdx.x)) {
     if (threadIdx.x == 0) prm.plan[blockIdx.x] = CutPlan{};
     grid_dependency_wait();
     return;
   }
   const Guard g{abort_flag, prm.b.status};
-  DecodeWalk w;
-  w.start(prm, share, blockIdx.x);
   if (threadIdx.x == 0) {
     const int row0 = w.item / prm.b.Hkv * prm.rows;
     prm.plan[blockIdx.x] = CutPlan{share.per, w.t0, w.d.tiles, w.item % prm.b.Hkv, row0,

@@ -7,7 +7,7 @@
 //   Rows.  The R = rows * G (token, query head) pairs that read one key/value head are the rows, so a key
 //     tile is read once for all G heads; 256 of them are a pair of tiles.
 //   Work.  A CTA per SM walks an equal share of all (sequence, key/value head, pair) items' key tiles laid
-//     end to end, so neither a batch of ragged prompts nor a single chunk of few pairs leaves SMs idle; an
+//     end to end, each item with kPreItemCost units more for its start (Q) and end (O), so neither a batch of ragged prompts nor a single chunk of few pairs leaves SMs idle; an
 //     item that a cut divides leaves unnormalised fp32 sums for the join.  The number of tiles that a pair
 //     sees under the causal mask is a floor of a linear function, whose sums have a closed form, so every
 //     CTA finds its share by itself.
@@ -33,6 +33,7 @@ constexpr int kSitePrefill = 0xC00;
 constexpr int kPreCtas = 148;
 constexpr int kPreRows = 256;     // query rows of an item: two tiles
 constexpr int kPreMinTiles = 2;   // a CTA's share is at least this many key tiles
+constexpr int kPreItemCost = 4;   // key tiles' worth of time that starting and ending an item takes
 
 // Register split (setmaxnreg), the launch's total.  The issuing thread keeps its loop state and the
 // descriptors that the compiler holds: at the contiguous forward's 56 it spilled 28 words and reloaded them
@@ -134,14 +135,15 @@ struct PrefillSeq {
   int linear;      // pair p counts (x + 2 p) / G + 1 tiles, the last one all; otherwise every pair counts all
   int x;
   int G;
-  // Tiles counted before pair p (p < pairs), and pair p's own; a pair's rows see no tile beyond its own.
+  // Units counted before pair p (p < pairs), and pair p's tiles; a pair's rows see no tile beyond its own.
   FA_HD long long before(int p) const {
-    return linear ? p + floor_sum(p, G, 2, x) : static_cast<long long>(p) * tiles;
+    return static_cast<long long>(p) * kPreItemCost +
+           (linear ? p + floor_sum(p, G, 2, x) : static_cast<long long>(p) * tiles);
   }
   FA_HD int count(int p) const {
     return linear && p < pairs - 1 ? static_cast<int>((x + 2 * p) / G) + 1 : tiles;
   }
-  FA_HD long long head_units() const { return pairs == 0 ? 0 : before(pairs - 1) + tiles; }
+  FA_HD long long head_units() const { return pairs == 0 ? 0 : before(pairs - 1) + tiles + kPreItemCost; }
 };
 FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   PrefillSeq d;
@@ -158,27 +160,48 @@ FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
 }
 FA_HD long long prefill_per(long long total) {
   const long long per = (total + kPreCtas - 1) / kPreCtas;
-  return per < kPreMinTiles ? kPreMinTiles : per;
+  return per < kPreMinTiles + kPreItemCost ? kPreMinTiles + kPreItemCost : per;
 }
-// Unit `off` of a sequence: head, pair and tile.
+// Unit `off` of a sequence: head, pair and unit of the item.
 struct PrefillAt {
-  int h, p, tile;
+  int h, p, unit;
 };
-FA_HD PrefillAt prefill_at(const PrefillSeq& d, long long off) {
+template <typename F>
+FA_HD PrefillAt prefill_at(const PrefillSeq& d, long long off, const F& find) {
   PrefillAt a;
   const long long head = d.head_units();
   a.h = static_cast<int>(off / head);
-  const long long r = off % head;
-  int lo = 0, hi = d.pairs - 1;  // the last pair that begins at r or before
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (d.before(mid) <= r) lo = mid;
-    else hi = mid - 1;
-  }
-  a.p = lo;
-  a.tile = static_cast<int>(r - d.before(lo));
+  const long long r = off - a.h * head;
+  a.p = find(d, r);
+  a.unit = static_cast<int>(r - d.before(a.p));
   return a;
 }
+// The last pair that begins at unit r of a head or before: by halving, and by a warp's lanes together.
+struct FindPairAlone {
+  FA_HD int operator()(const PrefillSeq& d, long long r) const {
+    int lo = 0, hi = d.pairs - 1;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (d.before(mid) <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+struct FindPairWarp {
+  __device__ __forceinline__ int operator()(const PrefillSeq& d, long long r) const {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = d.pairs;  // in [lo, lo + n)
+    while (n > 1) {
+      const int step = (n + 31) / 32, p = lo + lane * step;
+      const uint32_t yes = __ballot_sync(0xffffffffu, lane * step < n && d.before(p) <= r);  // lane 0's always
+      const int last = 31 - __clz(yes);
+      n = min(step, n - last * step);
+      lo += last * step;
+    }
+    return lo;
+  }
+};
 
 struct PrefillShare {
   long long total, per, off;
@@ -233,40 +256,46 @@ __device__ __forceinline__ PrefillShare prefill_share(const PrefillParams& p, in
 
 // Walks a CTA's share: one segment (key tiles [t0, t1) of an item) after another.
 struct PrefillWalk {
-  long long left;
-  int b, h, p, t0, t1, n;  // n: the item's tiles
+  long long left;  // units
+  int b, h, p, u0, t0, t1, n;  // n: the item's tiles
   bool whole;
   PrefillSeq d;
-  FA_HD void start(const PrefillParams& prm, const PrefillShare& s, int index) {
+  // False when the share holds no tile.
+  template <typename F>
+  FA_HD bool start(const PrefillParams& prm, const PrefillShare& s, int index, const F& find) {
     left = min(s.per, s.total - s.per * index);
     b = s.b;
     d = prefill_seq(prm, b);
-    const PrefillAt a = prefill_at(d, s.off);
+    const PrefillAt a = prefill_at(d, s.off, find);
     h = a.h;
     p = a.p;
-    t0 = a.tile;
+    u0 = a.unit;
     cut();
+    return t1 > 0 || next(prm);
   }
   FA_HD void cut() {
     n = d.count(p);
-    t1 = static_cast<int>(min(static_cast<long long>(n), t0 + left));
+    t0 = max(0, u0 - kPreItemCost);
+    t1 = max(0, static_cast<int>(min(static_cast<long long>(n + kPreItemCost), u0 + left)) - kPreItemCost);
     whole = t0 == 0 && t1 == n;
   }
   FA_HD bool next(const PrefillParams& prm) {
-    left -= t1 - t0;
-    if (left <= 0) return false;
-    t0 = 0;
-    if (++p == d.pairs) {
-      p = 0;
-      if (++h == prm.b.Hkv) {
-        h = 0;
-        do {
-          if (++b >= prm.b.B) return false;
-          d = prefill_seq(prm, b);
-        } while (d.pairs == 0);
+    do {
+      left -= n + kPreItemCost - u0;
+      if (left <= 0) return false;
+      u0 = 0;
+      if (++p == d.pairs) {
+        p = 0;
+        if (++h == prm.b.Hkv) {
+          h = 0;
+          do {
+            if (++b >= prm.b.B) return false;
+            d = prefill_seq(prm, b);
+          } while (d.pairs == 0);
+        }
       }
-    }
-    cut();
+      cut();
+    } while (t1 == 0);
     return true;
   }
   // The first key tile that query tile t does not see within this segment (t0: it sees none of it).
@@ -387,13 +416,13 @@ __global__ void __launch_bounds__(384, 1)
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
       PrefillWalk w;
-      w.start(prm, share, blockIdx.x);
+      bool ok = true, more = w.start(prm, share, blockIdx.x, FindPairWarp{});
       if (lane == 0)
-        prm.plan[blockIdx.x] = CutPlan{share.per, w.t0, w.n, w.h, w.p * kPreRows,
-                                       min(kPreRows, w.d.s.rows * prm.G - w.p * kPreRows), w.d.s.row0};
+        prm.plan[blockIdx.x] = more ? CutPlan{share.per, w.t0, w.n, w.h, w.p * kPreRows,
+                                              min(kPreRows, w.d.s.rows * prm.G - w.p * kPreRows), w.d.s.row0}
+                                    : CutPlan{};
       const int shift = min(prm.b.page_shift, 7), box_rows = 1 << shift;
       constexpr int kCols = FP8 ? D : 64;
-      bool ok = true, more = true;
       int kt = 0, kn = 0, vn = 0;  // key tiles since the start, loads issued
       while (ok) {
         const int si = seg_n % L::kSegs;
@@ -641,52 +670,62 @@ __global__ void __launch_bounds__(384, 1)
       const int lim = prm.causal && real ? len - w->rows + token : len - 1;  // last visible key
       const int lim_min = prm.causal ? len - w->rows + (w->p * kPreRows + t * kTile) / prm.G : len - 1;
       float sl2 = prm.scale_log2;
+      // Rows go between global and shared memory by the warp, LPR lanes a row, so that a load or store covers
+      // whole lines (a thread a row took 32 lines an instruction: 4 us a segment for Q, as much for O).
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of an instruction
+      const int chunk = lane % LPR, sub = lane / LPR;
+      const uint32_t reals = __ballot_sync(0xffffffffu, real);
       if (end > t0) {
-        // this thread's row of Q; the tile's last S is done, since this thread has seen its scores
-        const uint4* q = reinterpret_cast<const uint4*>(prm.Q + static_cast<size_t>(w->row0 + token) * prm.ldq + head * D);
-        uint4 x[D / 8];
+        // the tile's last S is done, since these threads have seen its scores
+        const __nv_bfloat16* mine = prm.Q + (real ? static_cast<size_t>(w->row0 + token) * prm.ldq + head * D : 0);
+        uint4 x[LPR];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = real ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (FP8) {
-          float amax = 0.0f;
+        for (int i = 0; i < LPR; ++i) {
+          const int from = i * RPI + sub;
+          const auto* q = reinterpret_cast<const __nv_bfloat16*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
+          x[i] = (reals >> from) & 1 ? __ldg(reinterpret_cast<const uint4*>(q) + chunk) : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < LPR; ++i) {
+          const int row = quarter * 32 + i * RPI + sub;  // of the tile
+          uint8_t* to = smem + L::kQ + t * L::kQBytes;
+          if constexpr (FP8) {
             const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
-          }
-          // q * 256 / (a power of two above the row's largest magnitude) = first part + second part, both e4m3
-          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 252);
-          sl2 *= __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t part[2][4];
+            float f[8], amax = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint4& y = x[2 * i + (k >> 1)];
-              const uint32_t v0 = k & 1 ? y.z : y.x, v1 = k & 1 ? y.w : y.y;
-              const float f[4] = {__uint_as_float(v0 << 16) * down, __uint_as_float(v0 & 0xFFFF0000u) * down,
-                                  __uint_as_float(v1 << 16) * down, __uint_as_float(v1 & 0xFFFF0000u) * down};
-              part[0][k] = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+              f[2 * k] = __uint_as_float(v[k] << 16);
+              f[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u);
+              amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+            }
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // q * 256 / (a power of two above the row's largest magnitude) = first part + second part, both e4m3
+            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 252);
+            const float down = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
+            const int e_row = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);  // for the row's own thread
+            if (i == lane / RPI) sl2 = prm.scale_log2 * __uint_as_float(static_cast<uint32_t>(e_row - 8) << 23);
+            uint32_t part[2][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int n = 0; n < 4; ++n) f[4 * k + n] *= down;
+              part[0][k] = e4m3x2(f[4 * k], f[4 * k + 1]) | (e4m3x2(f[4 * k + 2], f[4 * k + 3]) << 16);
               uint32_t h0, h1;
               halves_of_e4m3(part[0][k], h0, h1);
               const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
               const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-              part[1][k] = e4m3x2(f[0] - a.x, f[1] - a.y) | (e4m3x2(f[2] - b.x, f[3] - b.y) << 16);
+              part[1][k] = e4m3x2(f[4 * k] - a.x, f[4 * k + 1] - a.y) |
+                           (e4m3x2(f[4 * k + 2] - b.x, f[4 * k + 3] - b.y) << 16);
             }
-            const int at = D == 128 ? r * 128 + ((i ^ (r & 7)) << 4) : r * 64 + ((i ^ ((r >> 1) & 3)) << 4);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-              *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kQBytes + n * (kTile * D) + at) =
-                  make_uint4(part[n][0], part[n][1], part[n][2], part[n][3]);
+            const int c = chunk >> 1;  // 16 bytes are two lanes' eight codes
+            to += (D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4)) + (chunk & 1) * 8;
+            *reinterpret_cast<uint2*>(to) = make_uint2(part[0][0], part[0][1]);
+            *reinterpret_cast<uint2*>(to + kTile * D) = make_uint2(part[1][0], part[1][1]);
+          } else {
+            *reinterpret_cast<uint4*>(to + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = x[i];
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint4*>(smem + L::kQ + t * L::kQBytes + (i >> 3) * 16384 + r * 128 +
-                                      (((i & 7) ^ (r & 7)) << 4)) = x[i];
         }
         fence_proxy_async();
         mbar_arrive(&q_full[t]);
@@ -750,7 +789,7 @@ __global__ void __launch_bounds__(384, 1)
         float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
         // P, 32 keys -> 16 columns at a time, over S
         auto exp_store = [&](auto tiny_tag) {
-          constexpr bool kTiny = decltype(tiny_tag)::value;
+          [[maybe_unused]] constexpr bool kTiny = decltype(tiny_tag)::value;
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
             uint32_t pk[16];
@@ -821,27 +860,47 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 14))) break;
         tc_fence_after();
         const float scale = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        // rows of W bytes through the tile's part of Q, which no MMA reads any more: results in one go, parts
+        // (fp32, twice as wide) in two
+        constexpr int W = 2 * D;
+        uint8_t* stage = smem + L::kQ + t * L::kQBytes + quarter * (32 * W);
+        const auto mine = reinterpret_cast<unsigned long long>(whole ? static_cast<void*>(prm.O + at * D)
+                                                                     : static_cast<void*>(prm.part_o + slot * D));
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-          reg_fence(o);
-          if (real && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(prm.O + at * D + 32 * c);
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[4];
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + (D / 2) * half + 32 * c, o);
+            tmem_wait_ld();
+            reg_fence(o);
+            if (whole) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * scale, __uint_as_float(o[8 * i + 2 * k + 1]) * scale);
-              dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * scale, __uint_as_float(o[8 * i + 2 * k + 1]) * scale);
+                const int k = (D / 16) * half + 4 * c + i;
+                *reinterpret_cast<uint4*>(stage + lane * W + ((k ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(stage + lane * W + (((8 * c + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
-          } else if (real) {
-            uint4* dst = reinterpret_cast<uint4*>(prm.part_o + slot * D + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
+          if (whole && half == 0) continue;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < LPR; ++i) {
+            const int from = i * RPI + sub;
+            auto* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, from));
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + from * W + ((chunk ^ (from & 7)) << 4));
+            if ((reals >> from) & 1) *reinterpret_cast<uint4*>(to + (whole ? 0 : half * W) + chunk * 16) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       } else if (real && whole) {  // no key is visible to any row of the tile

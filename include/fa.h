@@ -312,6 +312,10 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
  * row of its sequence.  For an e4m3 cache any scales >= 0 serve (value scales
  * below 2^-100 count as 2^-100, and they should not exceed 2^60).
  *
+ * Where a sequence's keys are cut for the GPU's SMs depends on the lengths of
+ * the whole batch: the same batch gives the same bits, another batch may round
+ * a sequence's results differently.
+ *
  * workspace: device memory of at least fa_fwd_paged_workspace_size() bytes,
  * 16-byte aligned; contents on entry do not matter, and calls that may overlap
  * in time must not share one (two captured graphs included).  The size depends

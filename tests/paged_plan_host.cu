@@ -98,8 +98,7 @@ static void shares(std::mt19937& rng, bool whole) {
     const DecodeShare s = locate(c);
     if (s.b >= B) continue;
     DecodeWalk w;
-    w.start(p, s, c);
-    do {
+    if (w.start(p, s, c)) do {
       REQUIRE(w.item >= 0 && w.item < w.d.items && w.t0 >= 0 && w.t0 < w.t1 && w.t1 <= w.d.tiles);
       auto& v = seen[{w.b, w.item}];
       v.resize(w.d.tiles);
@@ -125,8 +124,7 @@ static void shares(std::mt19937& rng, bool whole) {
     const DecodeShare s = locate(c);
     if (s.b >= B) continue;
     DecodeWalk w;
-    w.start(p, s, c);
-    if (w.t0 == 0) continue;
+    if (!w.start(p, s, c) || w.t0 == 0) continue;
     const Cut cut = cut_of(per, c, w.t0, w.d.tiles);
     REQUIRE(cut.last >= c && cut.first < c);
     if (cut.first != c - 1) continue;
@@ -173,7 +171,7 @@ static void many_rows(std::mt19937& rng) {
     long long sum = 0;
     for (int k = 0; k < d.pairs; ++k) {
       REQUIRE(d.before(k) == sum);
-      sum += d.count(k);
+      sum += d.count(k) + kPreItemCost;
       // a pair's rows see none but its own tiles
       const int last_row = std::min((k + 1) * kPreRows, d.s.rows * p.G) - 1;
       const int last = p.causal ? d.s.len - d.s.rows + last_row / p.G : d.s.len - 1;
@@ -203,8 +201,7 @@ static void many_rows(std::mt19937& rng) {
     const PrefillShare s = locate(c);
     if (s.b >= B) continue;
     PrefillWalk w;
-    w.start(p, s, c);
-    do {
+    if (w.start(p, s, c, FindPairAlone{})) do {
       REQUIRE(w.p >= 0 && w.p < w.d.pairs && w.h < p.b.Hkv && w.t0 >= 0 && w.t0 < w.t1 && w.t1 <= w.n);
       for (int t = 0; t < 2; ++t) {
         const int end = w.end(p, t), first = w.p * kPreRows + t * kTile;
@@ -235,8 +232,7 @@ static void many_rows(std::mt19937& rng) {
     const PrefillShare s = locate(c);
     if (s.b >= B) continue;
     PrefillWalk w;
-    w.start(p, s, c);
-    if (w.t0 == 0) continue;
+    if (!w.start(p, s, c, FindPairAlone{}) || w.t0 == 0) continue;
     const Cut cut = cut_of(per, c, w.t0, w.n);
     REQUIRE(cut.last >= c && cut.first < c);
     if (cut.first != c - 1) continue;

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from exact_attention_159_b200 import _lib, api, build
-from tests.paged_util import E4M3, Batch, check, e4m3_round, needed_scale, rotate
+from tests.paged_util import E4M3, Batch, check, e4m3_round, needed_scale, reference, rotate
 
 pytestmark = pytest.mark.gpu
 
@@ -180,7 +180,6 @@ def _status():
 def test_bad_indices_are_recorded_and_leave_the_other_sequences_right(e4m3, q_lens):
     lens = [260, 64, 200]
     base = Batch(q_lens, lens, 8, 2, 128, 16, e4m3, seed=41)
-    good = [0, 2]
 
     def run(change):
         cache, batch, q = base.dev()
@@ -190,23 +189,29 @@ def test_bad_indices_are_recorded_and_leave_the_other_sequences_right(e4m3, q_le
         api.fa_fwd_paged(q, cache, batch, 0.1, True, out=out, lse=lse)
         return _status(), out, lse
 
-    st, ref_o, ref_l = run(lambda b: None)
-    assert st == (0, 0)
+    # the other sequences' results are right, not the same bits: where a sequence's keys are cut depends on
+    # the lengths of all
+    O, L, tO, tL = reference(base, 0.1, True)
+
+    def right(out, lse, b):
+        rows = slice(int(base.cu_q[b]), int(base.cu_q[b + 1]))
+        return (bool(((out[rows].double().cpu() - O[rows]).abs() <= tO[rows]).all())
+                and bool(((lse[rows].double().cpu() - L[rows]).abs() <= tL[rows]).all()))
+
+    st, out, lse = run(lambda b: None)
+    assert st == (0, 0) and all(right(out, lse, b) for b in range(3))
     for what, change in ((0xE03, lambda b: b.block_table[1].fill_(base.n_pages)),
                          (0xE03, lambda b: b.block_table[1].fill_(-1)),
                          (0xE03, lambda b: b.block_table[1].fill_(2 ** 31 - 1)),
                          (0xE02, lambda b: b.seq_lens[1].fill_(-3)),
-                         (0xE02, lambda b: b.seq_lens[1].fill_(2 ** 31 - 1)),
-                         ):
+                         (0xE02, lambda b: b.seq_lens[1].fill_(2 ** 31 - 1))):
         (rc, detail), out, lse = run(change)
         # a length far beyond the table is cut to it, where the entries behind the last token may be bad pages too
         assert rc == _lib.FA_ERR_INDEX and detail in (what, 0xE03), hex(detail)
-        for b in good:
-            rows = slice(int(base.cu_q[b]), int(base.cu_q[b + 1]))
-            assert torch.equal(out[rows], ref_o[rows]) and torch.equal(lse[rows], ref_l[rows])
+        assert right(out, lse, 0) and right(out, lse, 2)
     (rc, detail), out, lse = run(lambda b: b.cu_q[3].fill_(base.T + 1))
     assert (rc, detail) == (_lib.FA_ERR_INDEX, 0xE01)
-    assert torch.equal(out[: int(base.cu_q[2])], ref_o[: int(base.cu_q[2])]) and bool((out[int(base.cu_q[2]):] == 0).all())
+    assert right(out, lse, 0) and right(out, lse, 1) and bool((out[int(base.cu_q[2]):] == 0).all())
     (rc, detail), out, lse = run(lambda b: b.cu_q[0].fill_(-1))
     assert (rc, detail) == (_lib.FA_ERR_INDEX, 0xE01)
     assert _status() == (0, 0)
