@@ -257,6 +257,7 @@ class PagedCache:
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.d = pages, heads, size, d
         self.device = k_pages.device
+        self._index = k_pages.get_device()
         self._c = _lib.CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr() if fp8 else None,
                                    v_scale.data_ptr() if fp8 else None,
                                    _lib.FA_CACHE_E4M3 if fp8 else _lib.FA_CACHE_BF16, pages, heads, size, d)
@@ -280,6 +281,7 @@ class PagedBatch:
         self.block_table, self.cu_q, self.seq_lens = block_table, cu_q, seq_lens
         self.B, self.max_pages, self.max_q = B, max_pages, int(max_q)
         self.device = block_table.device
+        self._index = block_table.get_device()
         self._c = _lib.BatchStruct(block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), B, max_pages,
                                    self.max_q)
         self._ref = ctypes.byref(self._c)
@@ -287,13 +289,11 @@ class PagedBatch:
 
 def _need_rows(t: torch.Tensor, name: str, heads: int, d: int, rows: int, device: int) -> int:
     """Checks token-major rows [rows, heads, d] with each row contiguous; returns the elements between rows."""
-    if t.dtype != _BF16 or not t.is_cuda or tuple(t.shape) != (rows, heads, d):
-        raise ValueError(f"{name}: expected CUDA {_BF16} {(rows, heads, d)}, got {t.dtype} {tuple(t.shape)} "
-                         f"cuda={t.is_cuda}")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
+    if t.dtype != _BF16 or t.shape != (rows, heads, d) or t.get_device() != device:
+        raise ValueError(f"{name}: expected {_BF16} {(rows, heads, d)} on the current device cuda:{device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     row, head, col = t.stride()
-    if rows > 0 and heads > 0 and (col != 1 or (heads > 1 and head != d)):
+    if (col != 1 or head != d) and rows > 0 and heads > 0 and (col != 1 or heads > 1):
         raise ValueError(f"{name}: expected each token's {heads} x {d} elements contiguous, got strides {t.stride()}")
     return row if rows > 1 else heads * d
 
@@ -310,20 +310,19 @@ def _on_stream(stream):
                              else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
 
 
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor for a call on `stream` (None: the current one), whose memory that stream reuses."""
+def _empty(like, shape, dtype, stream):
+    """An uninitialised tensor on like's device for a call on `stream` (None: the current one), whose memory that
+    stream reuses."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with _on_stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _same_device(cache: PagedCache, batch: PagedBatch) -> int:
     """The current device, which the cache and the batch have to be on."""
-    if not torch.cuda.is_initialized():
-        raise ValueError("expected CUDA tensors")
     cur = torch._C._cuda_getDevice()
-    if cache.device.index != cur or batch.device.index != cur:
+    if cache._index != cur or batch._index != cur:
         raise ValueError(f"cache on {cache.device}, batch on {batch.device}, but the current device is cuda:{cur}")
     return cur
 
@@ -359,7 +358,7 @@ def fa_cache_append(k, v, cache: PagedCache, batch: PagedBatch, cos=None, sin=No
         if heads == 0 or Hq % heads:
             raise ValueError(f"q: {Hq} heads over {heads} key/value heads")
         if q_out is None:
-            q_out = _empty((T, Hq, d), _BF16, q.device, stream)
+            q_out = _empty(q, (T, Hq, d), _BF16, stream)
             ldqo = Hq * d
         else:
             ldqo = _need_rows(q_out, "q_out", Hq, d, T, cur)
@@ -390,17 +389,17 @@ def fa_fwd_paged(q, cache: PagedCache, batch: PagedBatch, scale: float | None = 
     lib = _lib.lib()
     ws_bytes = lib.fa_fwd_paged_workspace_size(cache._ref, batch._ref, T, Hq)
     if workspace is None:
-        workspace = _empty((max(ws_bytes, 16),), torch.uint8, q.device, stream)
+        workspace = _empty(q, (max(ws_bytes, 16),), torch.uint8, stream)
         ws_bytes = max(ws_bytes, 16)
     else:
         _need_workspace(workspace, ws_bytes)
         ws_bytes = workspace.numel() * workspace.element_size()
     if out is None:
-        out = _empty((T, Hq, d), _BF16, q.device, stream)
+        out = _empty(q, (T, Hq, d), _BF16, stream)
     else:
         _need(out, "out", _BF16, (T, Hq, d))
     if lse is None:
-        lse = _empty((T, Hq), torch.float32, q.device, stream)
+        lse = _empty(q, (T, Hq), torch.float32, stream)
     else:
         _need(lse, "lse", torch.float32, (T, Hq))
     check(lib.fa_fwd_paged(q.data_ptr(), ldq, cache._ref, batch._ref, T, out.data_ptr(), lse.data_ptr(),

@@ -23,8 +23,12 @@ namespace {
 // takes whole items and nothing is joined.
 constexpr int kWholeKeys = 256;
 // Sequences of at most this many rows (new tokens x query heads of a key/value head) go to the kernel of few
-// rows, longer ones to the tensor-core tiles.
-constexpr int kDecodeMaxRows = 32;
+// rows, longer ones to the tensor-core tiles, whose time hardly depends on the rows up to 128.  24 sequences
+// of 4096 keys, 8 x 4 heads, and one of 65536, few rows against tiles: e4m3 at 32 rows 91 / 117 us and 72 / 79
+// us, at 48 rows 119 / 117 us and 93 / 81 us; bf16 at 16 rows 81 / 100 us and 59 / 79 us, at 24 rows 94 / 101 us
+// and 98 / 80 us.
+constexpr int kDecodeMaxRowsBf16 = 16, kDecodeMaxRowsE4m3 = 32;
+int decode_max_rows(const fa_paged_cache* c) { return c->type == FA_CACHE_E4M3 ? kDecodeMaxRowsE4m3 : kDecodeMaxRowsBf16; }
 
 struct Sizes {
   size_t cache, scales, table;
@@ -151,8 +155,8 @@ PagedWs paged_ws(int d, bool many) {
   w.total = at;
   return w;
 }
-bool many_rows(const fa_paged_batch* b, int T, int G) {
-  return static_cast<long long>(b->max_q < T ? b->max_q : T) * G > kDecodeMaxRows;
+bool many_rows(const fa_paged_cache* c, const fa_paged_batch* b, int T, int G) {
+  return static_cast<long long>(b->max_q < T ? b->max_q : T) * G > decode_max_rows(c);
 }
 bool whole_items(const fa_paged_cache* c, const fa_paged_batch* b) {
   return static_cast<long long>(b->max_pages) * c->page_size <= kWholeKeys;
@@ -289,7 +293,7 @@ size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_b
   bool empty = false;
   Sizes z;
   if (check_paged(cache, batch, T, Hq, true, &empty, &z) != FA_OK || empty) return 0;
-  return paged_ws(cache->d, many_rows(batch, T, Hq / cache->heads)).total;
+  return paged_ws(cache->d, many_rows(cache, batch, T, Hq / cache->heads)).total;
 }
 
 int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const fa_paged_batch* batch, int T, void* O,
@@ -305,7 +309,7 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   if (ldq % 8 || !aligned16(Q) || !aligned16(O) || !aligned16(LSE) || !aligned16(workspace)) return FA_ERR_ALIGNMENT;
   if (ldq > (1LL << 40) / T || static_cast<long long>(T) * Hq > INT_MAX) return FA_ERR_UNSUPPORTED;
   const int G = Hq / cache->heads;
-  const bool many = many_rows(batch, T, G);
+  const bool many = many_rows(cache, batch, T, G);
   const PagedWs ws = paged_ws(cache->d, many);
   if (workspace_bytes < ws.total) return FA_ERR_INVALID_ARG;
   const size_t qb = rows_bytes(T, ldq, Hq, cache->d), ob = static_cast<size_t>(T) * Hq * cache->d * 2;
@@ -343,7 +347,7 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   dec.tile = tile;
   // eight rows an item where single tokens fit them and are most of what comes; sixteen for a few tokens
   dec.rows = G <= 8 && (many || static_cast<long long>(batch->max_q) * G <= 8) ? 8 : 16;
-  dec.max_rows = kDecodeMaxRows;
+  dec.max_rows = decode_max_rows(cache);
   dec.causal = causal;
   dec.whole = whole_items(cache, batch) ? 1 : 0;
   dec.scale_log2 = scale * 1.4426950408889634f;
@@ -360,7 +364,7 @@ int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const 
   pre.part_ml = reinterpret_cast<float2*>(wsb + ws.pre_ml);
   pre.G = G;
   pre.Hq = Hq;
-  pre.min_rows = kDecodeMaxRows;
+  pre.min_rows = decode_max_rows(cache);
   pre.causal = causal;
   pre.scale_log2 = dec.scale_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -78,7 +78,8 @@ struct PrefillLayout {
   static constexpr int kSegs = 4;
   static constexpr int kNumBars = 2 + 2 * kStagesK + 3 * kStagesV + 6 + 1 + kRaws + 2 * kSegs;
   static constexpr int kSeg = kBar + kNumBars * 8 + (kNumBars & 1) * 8;
-  static constexpr int kMisc = kSeg + kSegs * 48;
+  static constexpr int kMl = kSeg + kSegs * 48;  // (m, l) of a split item's second half
+  static constexpr int kMisc = kMl + kTile * 8;
   static constexpr int kBytes = kMisc + 16 + 16 * 8;
   static constexpr int kThreads = 384;
   static constexpr int kLaunchRegs = (65536 / kThreads) / 8 * 8;
@@ -132,18 +133,21 @@ struct PrefillSeq {
   SeqInfo s;
   int pairs;       // 0: no rows, or too few for this kernel
   int tiles;       // key tiles of the whole sequence (1 when it has no key: its rows are written)
+  int half;        // the last pair has one tile of rows: its steps are two key tiles each
   int linear;      // pair p counts (x + 2 p) / G + 1 tiles, the last one all; otherwise every pair counts all
   int x;
   int G;
-  // Units counted before pair p (p < pairs), and pair p's tiles; a pair's rows see no tile beyond its own.
+  // Units counted before pair p (p < pairs), and pair p's steps (key tiles, or two of them); a pair's rows see no
+  // key beyond its own steps.
   FA_HD long long before(int p) const {
     return static_cast<long long>(p) * kPreItemCost +
            (linear ? p + floor_sum(p, G, 2, x) : static_cast<long long>(p) * tiles);
   }
   FA_HD int count(int p) const {
-    return linear && p < pairs - 1 ? static_cast<int>((x + 2 * p) / G) + 1 : tiles;
+    if (p == pairs - 1) return half ? (tiles + 1) / 2 : tiles;
+    return linear ? static_cast<int>((x + 2 * p) / G) + 1 : tiles;
   }
-  FA_HD long long head_units() const { return pairs == 0 ? 0 : before(pairs - 1) + tiles + kPreItemCost; }
+  FA_HD long long head_units() const { return pairs == 0 ? 0 : before(pairs - 1) + count(pairs - 1) + kPreItemCost; }
 };
 FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   PrefillSeq d;
@@ -152,6 +156,7 @@ FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   const long long rows = static_cast<long long>(d.s.rows) * p.G;
   d.pairs = rows > p.min_rows ? static_cast<int>((rows + kPreRows - 1) / kPreRows) : 0;
   d.tiles = max(1, (d.s.len + 127) / 128);
+  d.half = d.pairs > 0 && rows - static_cast<long long>(d.pairs - 1) * kPreRows <= kTile;
   // pair p's last row (when the pair is full) is token (256 (p + 1) - 1) / G, which sees keys up to len - rows +
   // that; a tile has 128 keys, and 256 p is a multiple of 128, which leaves (x + 2 p) / G
   d.linear = p.causal && d.s.len >= d.s.rows;
@@ -254,10 +259,10 @@ __device__ __forceinline__ PrefillShare prefill_share(const PrefillParams& p, in
   return r;
 }
 
-// Walks a CTA's share: one segment (key tiles [t0, t1) of an item) after another.
+// Walks a CTA's share: one segment (steps [t0, t1) of an item) after another.
 struct PrefillWalk {
   long long left;  // units
-  int b, h, p, u0, t0, t1, n;  // n: the item's tiles
+  int b, h, p, u0, t0, t1, n;  // t0, t1: steps; n: the item's steps
   bool whole;
   PrefillSeq d;
   // False when the share holds no tile.
@@ -298,14 +303,16 @@ struct PrefillWalk {
     } while (t1 == 0);
     return true;
   }
-  // The first key tile that query tile t does not see within this segment (t0: it sees none of it).
+  FA_HD bool split() const { return d.half && p == d.pairs - 1; }
+  FA_HD int first() const { return split() ? 2 * t0 : t0; }  // first key tile
+  // The first key tile that query tile t does not see within this segment (first(): it sees none of it).
   FA_HD int end(const PrefillParams& prm, int t) const {
-    const int rows = d.s.rows * prm.G, row0 = p * kPreRows + t * kTile;
-    if (row0 >= rows) return t0;
+    const int rows = d.s.rows * prm.G, row0 = p * kPreRows + (split() ? 0 : t * kTile);
+    if (row0 >= rows) return first();
     const int last_row = min(row0 + kTile, rows) - 1;
     const int last = prm.causal ? d.s.len - d.s.rows + last_row / prm.G : d.s.len - 1;
     const int seen = last < 0 ? 0 : min(last / kTile + 1, (d.s.len + kTile - 1) / kTile);
-    return max(t0, min(t1, seen));
+    return max(first(), min(split() ? 2 * t1 : t1, seen));
   }
 };
 
@@ -316,7 +323,9 @@ struct alignas(16) PrefillSegment {
   int t0;               // first key tile; below 0: the share is done
   int end[2];           // the first one that each query tile does not see
   int whole;            // the item is whole: results, not parts
-  int pad[3];
+  int split;            // one tile of rows: query tile t takes every second key tile from t0 + t
+  int step0;            // first step of the item
+  int pad;
 };
 static_assert(sizeof(PrefillSegment) == 48, "segment slots are 48 bytes");
 
@@ -436,14 +445,16 @@ __global__ void __launch_bounds__(384, 1)
           x.len = w.d.s.len;
           x.h = w.h;
           x.p = w.p;
-          x.t0 = more ? w.t0 : -1;
+          x.t0 = more ? w.first() : -1;
+          x.split = w.split();
+          x.step0 = w.t0;
           x.end[0] = w.end(prm, 0);
           x.end[1] = w.end(prm, 1);
           x.whole = w.whole;
           mbar_arrive(&seg_full[si]);
         }
         if (!more) break;
-        for (int j = w.t0; j < end && ok; ++j, ++kt) {
+        for (int j = w.first(); j < end && ok; ++j, ++kt) {
           const int keys = min(kTile, w.d.s.len - j * kTile);
           const int boxes = (keys + box_rows - 1) >> shift;
           int z = 0, y = 0;
@@ -530,8 +541,47 @@ __global__ void __launch_bounds__(384, 1)
         while (const PrefillSegment* w = segment(ok, kThread)) {
           const int t0 = w->t0, end0 = w->end[0], end1 = w->end[1];
           const int last = max(end0, end1);
+          const bool split = w->split;
           segment_done(true);
           if (last == t0) continue;
+          if (split) {
+            // key tile i of the segment is query tile (i & 1)'s alone: S two tiles ahead of P V
+            const int n = last - t0;
+            auto score = [&](int i) {
+              const int t = i & 1, s = (kt + i) % SK;
+              if (i < 2) {
+                if (!(ok = wait(&q_full[t], (q_ph >> t) & 1, g, kSitePrefill | 4))) return;
+                q_ph ^= 1u << t;
+              }
+              if (!(ok = wait(&k_full[s], ((kt + i) / SK) & 1, g, kSitePrefill | 3))) return;
+              tc_fence_after();
+              issue_s(t, s);
+              tc_commit(&s_full[t]);
+              tc_commit(&k_empty[s]);
+            };
+            // a segment of one key tile leaves the second half's Q unused: its barrier still has to turn
+            if (n == 1) {
+              if (!(ok = wait(&q_full[1], (q_ph >> 1) & 1, g, kSitePrefill | 4))) break;
+              q_ph ^= 2u;
+            }
+            score(0);
+            if (ok && n > 1) score(1);
+#pragma unroll 1
+            for (int i = 0; ok && i < n; ++i) {
+              const int t = i & 1, s = (kt + i) % SV;
+              if (!(ok = wait(&v_full[s], ((kt + i) / SV) & 1, g, kSitePrefill | 5))) break;
+              if (!(ok = wait(&p_full[t], (p_ph >> t) & 1, g, kSitePrefill | 7))) break;
+              p_ph ^= 1u << t;
+              tc_fence_after();
+              issue_pv(t, s, i > 1);
+              tc_commit(&o_full[t]);
+              tc_commit(&v_empty[s]);
+              if (i + 2 < n) score(i + 2);
+            }
+            if (!ok) break;
+            kt += n;
+            continue;
+          }
           if (!(ok = wait(&k_full[kt % SK], (kt / SK) & 1, g, kSitePrefill | 3))) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
@@ -661,14 +711,18 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tO = tmem + 256 + D * t + lane_off;
     const float4* meta = reinterpret_cast<const float4*>(smem + L::kMeta);
     bool ok = true;
+    bool met = false;       // left by the softmax warps' common decision
     int step = 0, kt0 = 0;  // this tile's steps, key tiles of the CTA before the segment
     while (const PrefillSegment* w = segment(ok, kWarp)) {
       const int t0 = w->t0, end = w->end[t], len = w->len;
+      const bool split = w->split;
+      const int j0 = split ? t0 + t : t0, dj = split ? 2 : 1;  // this tile's key tiles: j0, j0 + dj, ... < end
       // this thread's row of the sequence's rows * G: its token and query head
-      int token = (w->p * kPreRows + t * kTile + r) / prm.G, head = (w->p * kPreRows + t * kTile + r) % prm.G + w->h * prm.G;
+      const int row0 = w->p * kPreRows + (split ? 0 : t * kTile);
+      const int token = (row0 + r) / prm.G, head = (row0 + r) % prm.G + w->h * prm.G;
       const bool real = token < w->rows;
       const int lim = prm.causal && real ? len - w->rows + token : len - 1;  // last visible key
-      const int lim_min = prm.causal ? len - w->rows + (w->p * kPreRows + t * kTile) / prm.G : len - 1;
+      const int lim_min = prm.causal ? len - w->rows + row0 / prm.G : len - 1;
       float sl2 = prm.scale_log2;
       // Rows go between global and shared memory by the warp, LPR lanes a row, so that a load or store covers
       // whole lines (a thread a row took 32 lines an instruction: 4 us a segment for Q, as much for O).
@@ -702,7 +756,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             // q * 256 / (a power of two above the row's largest magnitude) = first part + second part, both e4m3
-            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 252);
+            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 255);
             const float down = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
             const int e_row = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);  // for the row's own thread
             if (i == lane / RPI) sl2 = prm.scale_log2 * __uint_as_float(static_cast<uint32_t>(e_row - 8) << 23);
@@ -731,7 +785,7 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(&q_full[t]);
       }
       float m_ref = -INFINITY, l = 0.0f;
-      for (int j = t0; j < end; ++j, ++step) {
+      for (int j = j0; j < end; j += dj, ++step) {
         if (!(ok = wait_warp(&s_full[t], step & 1, g, kSitePrefill | 12))) break;
         tc_fence_after();
         uint32_t sr[4][32];
@@ -830,7 +884,7 @@ __global__ void __launch_bounds__(384, 1)
 #undef S
         const float2 ls = __fadd2_rn(ls0, ls1);
         l += ls.x + ls.y;
-        if (j > t0 && __any_sync(0xffffffffu, need)) {
+        if (j > j0 && __any_sync(0xffffffffu, need)) {
           // O_t *= alpha once the previous P.V has landed (before p_full lets the next one add to it)
           ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 13);
           tc_fence_after();
@@ -852,12 +906,63 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         mbar_arrive(&p_full[t]);
       }
+      if (ok && j0 < end) ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 14);
+      if (split && end > t0) {
+        // the second half's O, m and l through shared memory (the tiles of Q, which no MMA reads any more) into
+        // the first half's
+        tc_fence_after();
+        float4* ring = reinterpret_cast<float4*>(smem + L::kQ + r * (4 * D));
+        float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
+        if (ok && t == 1 && j0 < end) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              ring[(8 * c + i) ^ (r & 7)] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          }
+        }
+        if (t == 1) ml[r] = make_float2(m_ref, l);
+        if (!(ok = group_and(2, 256, ok))) {
+          met = true;
+          break;
+        }
+        if (t == 0 && t0 + 1 < end) {
+          const float2 other = ml[r];
+          const float m = fmaxf(m_ref, other.x), ms = m == -INFINITY ? 0.0f : m;
+          const float ca = exp2_sfu(m_ref - ms), cb = exp2_sfu(other.x - ms);
+          l = l * ca + other.y * cb;
+          m_ref = m;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = ring[(8 * c + i) ^ (r & 7)];
+              o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * ca + v.x * cb);
+              o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * ca + v.y * cb);
+              o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * ca + v.z * cb);
+              o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * ca + v.w * cb);
+            }
+            tmem_st32(tO + 32 * c, o);
+          }
+          tmem_wait_st();
+        }
+        named_barrier(2, 256);
+      }
       if (!ok) break;
+      const bool stores = !(split && t == 1);  // a split item's second half is in the first's
       const size_t at = static_cast<size_t>(w->row0 + token) * prm.Hq + head;
       const bool whole = w->whole;
-      const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, t0)) * kPreRows + t * kTile + r;
-      if (end > t0) {
-        if (!(ok = wait_warp(&o_full[t], (step - 1) & 1, g, kSitePrefill | 14))) break;
+      const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, w->step0)) * kPreRows + (split ? 0 : t * kTile) + r;
+      if (end > t0 && stores) {
         tc_fence_after();
         const float scale = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
         // rows of W bytes through the tile's part of Q, which no MMA reads any more: results in one go, parts
@@ -903,11 +1008,11 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
         }
         tc_fence_before();
-      } else if (real && whole) {  // no key is visible to any row of the tile
+      } else if (real && whole && stores) {  // no key is visible to any row of the tile
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(prm.O + at * D)[i] = make_uint4(0u, 0u, 0u, 0u);
       }
-      if (real) {
+      if (real && stores) {
         if (whole) prm.LSE[at] = l > 0.0f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
         else prm.part_ml[slot] = make_float2(m_ref, l);  // m = -inf: the join takes nothing from this part
       }
@@ -915,6 +1020,8 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       segment_done(lane == 0);
     }
+    // a warp that leaves on a failed wait of its own still meets those that wait for it in a split segment
+    if (!met) group_and(2, 256, ok);
   }
   tc_fence_before();
   __syncthreads();

@@ -176,8 +176,10 @@ static void many_rows(std::mt19937& rng) {
       const int last_row = std::min((k + 1) * kPreRows, d.s.rows * p.G) - 1;
       const int last = p.causal ? d.s.len - d.s.rows + last_row / p.G : d.s.len - 1;
       const int seen = last < 0 ? 0 : std::min(last, d.s.len - 1) / 128 + 1;
-      REQUIRE(d.count(k) >= std::max(seen, 1));
-      if (d.linear && seen > 0) REQUIRE(d.count(k) == seen);
+      const bool half = k == d.pairs - 1 && d.s.rows * p.G - k * kPreRows <= 128;
+      REQUIRE((k == d.pairs - 1 && d.half) == half);
+      REQUIRE(d.count(k) * (half ? 2 : 1) >= std::max(seen, 1));
+      if (d.linear && seen > 0) REQUIRE(d.count(k) == (half ? (seen + 1) / 2 : seen));
     }
     REQUIRE(d.head_units() == sum);
     units.push_back(sum * p.b.Hkv);
@@ -204,13 +206,15 @@ static void many_rows(std::mt19937& rng) {
     if (w.start(p, s, c, FindPairAlone{})) do {
       REQUIRE(w.p >= 0 && w.p < w.d.pairs && w.h < p.b.Hkv && w.t0 >= 0 && w.t0 < w.t1 && w.t1 <= w.n);
       for (int t = 0; t < 2; ++t) {
-        const int end = w.end(p, t), first = w.p * kPreRows + t * kTile;
-        REQUIRE(end >= w.t0 && end <= w.t1 && end * 128 < w.d.s.len + 128);
-        if (first >= w.d.s.rows * p.G) REQUIRE(end == w.t0);
+        const int f = w.split() ? 2 : 1, key0 = w.t0 * f, key1 = w.t1 * f;
+        const int end = w.end(p, t), first = w.p * kPreRows + (w.split() ? 0 : t * kTile);
+        REQUIRE(w.first() == key0 && end >= key0 && end <= key1 && (end == key0 || end * 128 < w.d.s.len + 128));
+        if (first >= w.d.s.rows * p.G) REQUIRE(end == key0);
+        if (w.split()) REQUIRE(w.end(p, 0) == w.end(p, 1) && w.d.s.rows * p.G - w.p * kPreRows <= 128);
         // every visible key of every row of the tile is in a tile below `end`, or in another segment
         for (int r = first; r < std::min(first + kTile, w.d.s.rows * p.G); ++r) {
           const int last = std::min(w.d.s.len - 1, p.causal ? w.d.s.len - w.d.s.rows + r / p.G : w.d.s.len - 1);
-          if (last >= w.t0 * 128) REQUIRE(end >= std::min(w.t1, last / 128 + 1));
+          if (last >= key0 * 128) REQUIRE(end >= std::min(key1, last / 128 + 1));
         }
       }
       auto& v = seen[{w.b, w.h, w.p}];

@@ -8,7 +8,10 @@ half's step is absolute, at most 2^-25 of the largest weight) and A = sum_j soft
   the output's rounding      2^-8 * |O|
   scores: d products summed in fp32 (each addition off by at most 2^-23 of the sum of magnitudes s1), the
     products with the factors, the exponent's argument and the approximate 2^x (2^-22): ds below, which moves
-    numerator and denominator alike, 2 * ds * A
+    numerator and denominator alike, 2 * ds * A.  For an e4m3 cache a query row is held as a power of two times
+    halves (off by 2^-25 of the row's largest magnitude) or two e4m3 parts (the second's least step is 2^-9 in units
+    where the largest is 128 to 256: off by half of that, at most 2^-17 of the largest): another
+    2^-17 max|q| sum|k| scale in ds
   sums and joins: fp32 relative 2^-23 per addition of a partial result, at most n_add of them
 LSE: ds + 2^-22 * (n_add + |LSE|).
 """
@@ -108,6 +111,8 @@ def reference(bt: Batch, scale, causal):
                 s1 = (q.abs() @ k.abs().T).amax(dim=1) * scale if n else torch.zeros(m, dtype=torch.float64)
                 top = torch.where(seen, s.abs(), 0.0).amax(dim=1) if n else torch.zeros(m, dtype=torch.float64)
                 ds = (d + 8) * 2.0 ** -23 * s1 + 2.0 ** -22 * (2 * top + 64)
+                if bt.e4m3 and n:
+                    ds = ds + 2.0 ** -17 * q.abs().amax(dim=1) * k.abs().sum(dim=1).max() * scale
                 n_add = 16 + n / 256
                 tiny = 0.0
                 if bt.e4m3 and n:  # halves below 2^-14 of the row's largest w_j = p_j * value scale

@@ -124,13 +124,39 @@ def test_scales_far_apart(q_lens, lens):
     check(bt, out, lse, scale, True, f"scales {q_lens}")
 
 
-@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** -30, 3.0e37])
-def test_queries_of_any_size(factor):
-    """An e4m3 cache's queries become halves by a power of two per row: none overflows or vanishes."""
-    bt = Batch([1, 3], [200, 129], 4, 1, 128, 64, True, seed=22)
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** -30, 2.0 ** -118, 3.0e37])
+@pytest.mark.parametrize("q_lens,lens", [([1, 3], [200, 129]), ([20, 70], [300, 129])])
+def test_queries_of_any_size(factor, q_lens, lens):
+    """An e4m3 cache's queries become halves, or two e4m3 parts, by a power of two per row: none overflows or
+    vanishes."""
+    bt = Batch(q_lens, lens, 4, 1, 128, 64, True, seed=22)
     bt.q = (bt.q.float() * factor).bfloat16()
     out, lse, scale = attend(bt, scale=1.0 / math.sqrt(128) / factor)
     check(bt, out, lse, scale, True, f"queries x {factor}")
+
+
+@pytest.mark.parametrize("q_lens,lens", [([1, 3], [200, 129]), ([20, 70], [300, 129])])
+def test_queries_with_outliers(q_lens, lens):
+    """A few columns of the queries 2^7 larger than the others, which still count."""
+    for d in (64, 128):
+        bt = Batch(q_lens, lens, 4, 1, d, 32, True, seed=23)
+        bt.q[..., 3::29] *= 128
+        bt.k.view(torch.uint8)[..., 3::29] &= 0x87  # and these columns of the keys among e4m3's subnormals
+        out, lse, scale = attend(bt)
+        check(bt, out, lse, scale, True, f"outliers d{d} {q_lens}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d,G", [(128, 4), (64, 8), (128, 1)])
+def test_row_counts_about_the_tiles(e4m3, d, G):
+    """Rows (new tokens x query heads) about 16, 32, 128, 256 and 384, over one to a few key tiles."""
+    counts = [16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257, 384, 385]
+    q_lens = sorted({-(-c // G) for c in counts})
+    lens = [q + extra for q, extra in zip(q_lens, [0, 1, 90, 128, 129, 300, 0, 7, 255, 256, 1000, 64, 3])]
+    bt = Batch(q_lens, lens, G, 1, d, 32, e4m3, seed=24)
+    for causal in (True, False):
+        out, lse, scale = attend(bt, causal)
+        check(bt, out, lse, scale, causal, f"row counts d{d} G{G} causal={causal} e4m3={e4m3}")
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
