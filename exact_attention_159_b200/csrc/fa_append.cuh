@@ -11,8 +11,8 @@
 // reuse the angles.  A thread holds 8 columns (16 bytes) of ITEMS tokens; a pair's other half is in
 // another lane of the same warp (a row is D / 8 consecutive lanes) and comes by shuffle, so every input is
 // read once and Q may be rotated in place.  What a block waits for is two dependent loads, the batch's
-// indices and then everything else at once (keys, values, angles, four query heads and the page number);
-// the rotated keys are not kept but rotated again after the maximum, which keeps four blocks on an SM.
+// indices and then everything else at once (keys, values, angles, four query heads and the page number); of
+// several tokens the rotated keys are not kept but rotated again after the maximum, for the registers' sake.
 // One or two new tokens a sequence (a decode batch) take blocks of one warp.  Bound by HBM for prompts
 // (each row is read once and written once), by the two loads' latency for single tokens.
 #pragma once
@@ -34,74 +34,94 @@ struct AppendParams {
   int max_touched;  // pages a sequence's new rows can touch
 };
 
-// Rotated fp32 values of this lane's 8 columns.  All 32 lanes call it together (shuffles).
-template <int D>
-__device__ __forceinline__ void rotate8(const uint4& raw, float (&x)[8], const float (&c)[8], const float (&s)[8],
-                                        int vec, int rot, int interleaved) {
-  constexpr int VPR = D / 8;
+// This lane's 8 columns as fp32 pairs.
+struct Eight {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ Eight unpack8(const uint4& raw) {
+  return Eight{{unpack2(raw.x), unpack2(raw.y), unpack2(raw.z), unpack2(raw.w)}};
+}
+
+// This lane's angles of one position: cosines and sines of its 8 columns (of its 4 pairs when interleaved),
+// the sines with the sign of the pair's first or second half.
+struct Angles {
+  float2 c[4], s[4];
+};
+__device__ __forceinline__ Angles load_angles(const AppendParams& prm, int p, int vec) {
+  const int half = prm.rot / 2;
+  const bool first = vec * 8 < half;
+  const size_t at = static_cast<size_t>(p) * half + (prm.interleaved ? vec * 4 : first ? vec * 8 : vec * 8 - half);
+  const float4* cp = reinterpret_cast<const float4*>(prm.cosp + at);
+  const float4* sp = reinterpret_cast<const float4*>(prm.sinp + at);
+  const float4 c0 = __ldg(cp), s0 = __ldg(sp);
+  Angles a;
+  if (prm.interleaved) {
+    a.c[0] = make_float2(c0.x, c0.x), a.c[1] = make_float2(c0.y, c0.y);
+    a.c[2] = make_float2(c0.z, c0.z), a.c[3] = make_float2(c0.w, c0.w);
+    a.s[0] = make_float2(-s0.x, s0.x), a.s[1] = make_float2(-s0.y, s0.y);
+    a.s[2] = make_float2(-s0.z, s0.z), a.s[3] = make_float2(-s0.w, s0.w);
+    return a;
+  }
+  const float4 c1 = __ldg(cp + 1), s1 = __ldg(sp + 1);
+  const float g = first ? -1.0f : 1.0f;
+  a.c[0] = make_float2(c0.x, c0.y), a.c[1] = make_float2(c0.z, c0.w);
+  a.c[2] = make_float2(c1.x, c1.y), a.c[3] = make_float2(c1.z, c1.w);
+  a.s[0] = make_float2(g * s0.x, g * s0.y), a.s[1] = make_float2(g * s0.z, g * s0.w);
+  a.s[2] = make_float2(g * s1.x, g * s1.y), a.s[3] = make_float2(g * s1.z, g * s1.w);
+  return a;
+}
+
+// Rotated values of this lane's 8 columns: x cos + (its pair's other half) sin.  All 32 lanes call it together;
+// `other` is the lane (of the row's VPR) with the other halves, `turns` whether this lane's columns are rotated.
+template <int VPR>
+__device__ __forceinline__ Eight rotate8(const uint4& raw, const Angles& a, int other, bool turns, bool interleaved) {
+  Eight x = unpack8(raw);
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-  if (rot == 0) return;
-  if (interleaved) {
-    if (vec * 8 < rot) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * c[i] - b * s[i];
-        x[2 * i + 1] = b * c[i] + a * s[i];
-      }
+    float2 o;
+    if (interleaved) {
+      o = make_float2(x.v[i].y, x.v[i].x);
+    } else {
+      o = unpack2(__shfl_sync(0xffffffffu, w[i], other, VPR));
     }
-    return;
+    if (turns) x.v[i] = __ffma2_rn(o, a.s[i], __fmul2_rn(x.v[i], a.c[i]));
   }
-  const int half = rot / 16;  // lanes of half the rotated columns
-  const int other = vec < half ? vec + half : vec < 2 * half ? vec - half : vec;
-  const float sign = vec < half ? -1.0f : 1.0f;
+  return x;
+}
+
+__device__ __forceinline__ uint4 pack8_bf16(const Eight& x) {
+  return make_uint4(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y),
+                    pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y));
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const Eight& x, float inv) {
+  const float2 f = make_float2(inv, inv);
+  uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t o = __shfl_sync(0xffffffffu, w[i], other, VPR);
-    if (vec < 2 * half) {
-      x[2 * i] = x[2 * i] * c[2 * i] + sign * __uint_as_float(o << 16) * s[2 * i];
-      x[2 * i + 1] = x[2 * i + 1] * c[2 * i + 1] + sign * __uint_as_float(o & 0xFFFF0000u) * s[2 * i + 1];
-    }
+    const float2 y = __fmul2_rn(x.v[i], f);
+    h[i] = e4m3x2(y.x, y.y);
   }
-}
-
-// This lane's table entries of position p (8 angles, 4 when interleaved).
-__device__ __forceinline__ void load_angles(const AppendParams& prm, int p, int vec, float (&c)[8], float (&s)[8]) {
-  const int half = prm.rot / 2;
-  const int first = prm.interleaved ? vec * 4 : (vec * 8 < half ? vec * 8 : vec * 8 - half);
-  const float4* cp = reinterpret_cast<const float4*>(prm.cosp + static_cast<size_t>(p) * half + first);
-  const float4* sp = reinterpret_cast<const float4*>(prm.sinp + static_cast<size_t>(p) * half + first);
-  const float4 c0 = __ldg(cp), s0 = __ldg(sp);
-  c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w;
-  s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w;
-  if (!prm.interleaved) {
-    const float4 c1 = __ldg(cp + 1), s1 = __ldg(sp + 1);
-    c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
-  }
-}
-
-__device__ __forceinline__ uint4 pack8_bf16(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
-  return make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16),
-                    e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16));
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 // The largest finite magnitude: an infinity saturates its own code and leaves the page's scale to the others.
-__device__ __forceinline__ float amax8(const float (&x)[8], float m) {
+// (NaN never wins a maximum; an infinity shows in the result, and only then is each value looked at.)
+__device__ __forceinline__ float amax8(const Eight& x, float m) {
+  float a = fmaxf(fabsf(x.v[0].x), fabsf(x.v[0].y));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(x[i]);
-    m = fmaxf(m, a < INFINITY ? a : 0.0f);
+  for (int i = 1; i < 4; ++i) a = fmax3(a, fabsf(x.v[i].x), fabsf(x.v[i].y));
+  if (!(a < INFINITY)) {
+    a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (fabsf(x.v[i].x) < INFINITY) a = fmaxf(a, fabsf(x.v[i].x));
+      if (fabsf(x.v[i].y) < INFINITY) a = fmaxf(a, fabsf(x.v[i].y));
+    }
   }
-  return m;
+  return fmaxf(m, a);
 }
 
 // Earlier codes of a page and head, `n` bytes (a multiple of 16), times ratio (below 1).
@@ -148,33 +168,41 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS ==
   const int first = max(start, base) - base, last = min(s.len, base + (1 << pb.page_shift)) - base;  // slots [first, last)
   const int vec = threadIdx.x % VPR, slot0 = first + threadIdx.x / VPR;
   const size_t row0 = static_cast<size_t>(s.row0 + base + slot0 - start);  // this thread's first token row
+  // the lane with the other halves of this lane's pairs, and whether its columns turn at all
+  const int half = prm.rot / 16;
+  const bool turns = vec * 8 < prm.rot, inter = prm.interleaved;
+  const int other = vec < half ? vec + half : vec < 2 * half ? vec - half : vec;
+  const __nv_bfloat16* kp = prm.K + row0 * prm.ldk + h * D + vec * 8;
+  const __nv_bfloat16* vp = prm.V + row0 * prm.ldv + h * D + vec * 8;
+  const __nv_bfloat16* qp = prm.Q + row0 * prm.ldq + h * prm.G * D + vec * 8;
+  __nv_bfloat16* qop = prm.Qo + row0 * prm.ldqo + h * prm.G * D + vec * 8;
+  const int limit = prm.rot > 0 ? min(last, prm.n_pos - base) : last;  // slots behind it are not written
 
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   uint4 kraw[ITEMS], vraw[ITEMS], qraw[kAppendQ];
-  auto live = [&](int i) { return slot0 + i * ROWS < last && (prm.rot == 0 || base + slot0 + i * ROWS < prm.n_pos); };
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const bool live = slot0 + i * ROWS < limit;
+    kraw[i] = live ? *reinterpret_cast<const uint4*>(kp + i * ROWS * prm.ldk) : zero;
+    vraw[i] = live ? *reinterpret_cast<const uint4*>(vp + i * ROWS * prm.ldv) : zero;
+  }
+  auto angles = [&](int i) {
+    Angles a;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a.c[j] = a.s[j] = make_float2(0.0f, 0.0f);
+    if (slot0 + i * ROWS < limit && turns) a = load_angles(prm, base + slot0 + i * ROWS, vec);
+    return a;
+  };
   auto load_q = [&](int i, int g0) {
 #pragma unroll
     for (int g = 0; g < kAppendQ; ++g)
-      qraw[g] = live(i) && g0 + g < prm.G
-                    ? *reinterpret_cast<const uint4*>(prm.Q + (row0 + i * ROWS) * prm.ldq + (h * prm.G + g0 + g) * D + vec * 8)
-                    : make_uint4(0u, 0u, 0u, 0u);
+      qraw[g] = slot0 + i * ROWS < limit && g0 + g < prm.G
+                    ? *reinterpret_cast<const uint4*>(qp + i * ROWS * prm.ldq + (g0 + g) * D)
+                    : zero;
   };
-  auto angles = [&](int i, float (&c)[8], float (&sn)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = sn[j] = 0.0f;
-    if (live(i) && vec * 8 < prm.rot) load_angles(prm, base + slot0 + i * ROWS, vec, c, sn);
-  };
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    kraw[i] = vraw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (live(i)) {
-      kraw[i] = *reinterpret_cast<const uint4*>(prm.K + (row0 + i * ROWS) * prm.ldk + h * D + vec * 8);
-      vraw[i] = *reinterpret_cast<const uint4*>(prm.V + (row0 + i * ROWS) * prm.ldv + h * D + vec * 8);
-    }
-    if (prm.rot > 0 && slot0 + i * ROWS < last && base + slot0 + i * ROWS >= prm.n_pos) record(pb.status, kBadPosition);
-  }
-  float c[8], sn[8];
-  angles(0, c, sn);
+  Angles ang = angles(0);
   load_q(0, 0);
+  if (limit < last && threadIdx.x == 0) record(pb.status, kBadPosition);
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(pb.num_pages)) {
     record(pb.status, kBadPage);
     return;
@@ -186,32 +214,29 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS ==
     ks_old = prm.Ks[static_cast<size_t>(page) * pb.Hkv + h];
     vs_old = prm.Vs[static_cast<size_t>(page) * pb.Hkv + h];
   }
+  Eight kx;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
+    const bool live = slot0 + i * ROWS < limit;
     if (i > 0) {
-      angles(i, c, sn);
+      ang = angles(i);
       load_q(i, 0);
     }
-    float x[8];
-    rotate8<D>(kraw[i], x, c, sn, vec, prm.rot, prm.interleaved);
+    kx = rotate8<VPR>(kraw[i], ang, other, turns, inter);
     if constexpr (FP8) {
-      ak = amax8(x, ak);
-      float vx[8];
-      rotate8<D>(vraw[i], vx, c, sn, vec, 0, 0);
-      av = amax8(vx, av);
-    } else if (live(i)) {
+      ak = amax8(kx, ak);
+      av = amax8(unpack8(vraw[i]), av);
+    } else if (live) {
       const size_t at = (head_at + slot0 + i * ROWS) * D + vec * 8;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Kc) + at) = pack8_bf16(x);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Kc) + at) = pack8_bf16(kx);
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Vc) + at) = vraw[i];
     }
     for (int g0 = 0; g0 < prm.G; g0 += kAppendQ) {
       if (g0 > 0) load_q(i, g0);
 #pragma unroll
       for (int g = 0; g < kAppendQ; ++g) {
-        rotate8<D>(qraw[g], x, c, sn, vec, prm.rot, prm.interleaved);
-        if (live(i) && g0 + g < prm.G)
-          *reinterpret_cast<uint4*>(prm.Qo + (row0 + i * ROWS) * prm.ldqo + (h * prm.G + g0 + g) * D + vec * 8) =
-              pack8_bf16(x);
+        const uint4 y = pack8_bf16(rotate8<VPR>(qraw[g], ang, other, turns, inter));
+        if (live && g0 + g < prm.G) *reinterpret_cast<uint4*>(qop + i * ROWS * prm.ldqo + (g0 + g) * D) = y;
       }
     }
   }
@@ -248,14 +273,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS ==
     const float ki = 1.0f / ks, vi = 1.0f / vs;  // exact for the powers of two written here
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      if (ITEMS > 1) angles(i, c, sn);
-      float x[8], vx[8];
-      rotate8<D>(kraw[i], x, c, sn, vec, prm.rot, prm.interleaved);
-      rotate8<D>(vraw[i], vx, c, sn, vec, 0, 0);
-      if (!live(i)) continue;
+      if (ITEMS > 1) {
+        ang = angles(i);
+        kx = rotate8<VPR>(kraw[i], ang, other, turns, inter);
+      }
+      if (slot0 + i * ROWS >= limit) continue;
       const size_t at = static_cast<size_t>(slot0 + i * ROWS) * D + vec * 8;
-      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(x, ki);
-      *reinterpret_cast<uint2*>(vc + at) = pack8_e4m3(vx, vi);
+      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(kx, ki);
+      *reinterpret_cast<uint2*>(vc + at) = pack8_e4m3(unpack8(vraw[i]), vi);
     }
   }
 }

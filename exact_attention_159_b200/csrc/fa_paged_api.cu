@@ -19,9 +19,12 @@ using namespace fa_host;
 
 namespace {
 
-// Short caches (at most this many keys by the block table's width) are not cut along the keys: each CTA
-// takes whole items and nothing is joined.
-constexpr int kWholeKeys = 256;
+// Short caches (by the block table's width) are not cut along the keys: each CTA takes whole items and
+// nothing is joined.  A step of 1, 32 and 128 sequences over 512 bf16 keys (8 x 4 heads), whole against cut:
+// 9.1 / 9.4, 10.7 / 15.7 and 50 / 53 us; over 1024 keys: 12.7 / 11.1, 26.9 / 31.8 and 93 / 91 us, so twice the
+// width where there are many items.
+constexpr int kWholeKeys = 512, kWholeItems = 64;
+
 // Sequences of at most this many rows (new tokens x query heads of a key/value head) go to the kernel of few
 // rows, longer ones to the tensor-core tiles, whose time hardly depends on the rows up to 128.  24 sequences
 // of 4096 keys, 8 x 4 heads, and one of 65536, few rows against tiles: e4m3 at 32 rows 91 / 117 us and 72 / 79
@@ -159,7 +162,8 @@ bool many_rows(const fa_paged_cache* c, const fa_paged_batch* b, int T, int G) {
   return static_cast<long long>(b->max_q < T ? b->max_q : T) * G > decode_max_rows(c);
 }
 bool whole_items(const fa_paged_cache* c, const fa_paged_batch* b) {
-  return static_cast<long long>(b->max_pages) * c->page_size <= kWholeKeys;
+  const long long keys = static_cast<long long>(b->max_pages) * c->page_size;
+  return keys <= (static_cast<long long>(b->B) * c->heads >= kWholeItems ? 2 * kWholeKeys : kWholeKeys);
 }
 
 struct FwdMaps {
