@@ -6,15 +6,17 @@
 //   scale' = max(scale of the page's earlier tokens, what the new values need), new codes e4m3(x / scale'),
 //   and, when the scale grew, the earlier codes brought to it: e4m3(code * scale / scale').
 //
-// A block owns one page of one sequence and one key/value head, since a page's scale is a maximum over all its
-// new tokens and growing it touches all its earlier ones; the G query heads of that head ride along and
-// reuse the angles.  A thread holds 8 columns (16 bytes) of ITEMS tokens; a pair's other half is in
-// another lane of the same warp (a row is D / 8 consecutive lanes) and comes by shuffle, so every input is
-// read once and Q may be rotated in place.  What a block waits for is two dependent loads, the batch's
-// indices and then everything else at once (keys, values, angles, four query heads and the page number); of
-// several tokens the rotated keys are not kept but rotated again after the maximum, for the registers' sake.
-// One or two new tokens a sequence (a decode batch) take blocks of one warp.  Bound by HBM for prompts
-// (each row is read once and written once), by the two loads' latency for single tokens.
+// A page's scale is a maximum over all its new tokens, and growing it touches all its earlier ones, so the unit
+// is one page of one sequence and one key/value head; the G query heads of that head ride along and reuse
+// the angles.  A block takes 16 tokens (D = 128; 32 at D = 64), a thread 8 columns (16 bytes) of one; the blocks
+// of a longer page are a cluster and exchange their maxima through shared memory (one block holding a whole
+// page had 148 to 245 registers a thread and reached 2.5 TB/s).  A pair's other half is in another lane of the
+// same warp (a row is D / 8 consecutive lanes) and comes by shuffle, so every input is read once and Q may be
+// rotated in place.  What a block waits for is two dependent loads, the batch's indices and then everything
+// else at once (keys, values, angles, four query heads and the page number); 64 registers keep four blocks on an
+// SM.  One or two new tokens a sequence (a decode batch) take blocks of one warp.  Bound by HBM for prompts
+// (each row is read once and written once) with the instruction rate close behind, by the two loads' latency
+// for single tokens.
 #pragma once
 
 #include "fa_paged.cuh"
@@ -32,6 +34,7 @@ struct AppendParams {
   float *Ks, *Vs;
   int G;          // query heads per key/value head (0: no queries)
   int max_touched;  // pages a sequence's new rows can touch
+  int subs;         // blocks of a page
 };
 
 // This lane's 8 columns as fp32 pairs.
@@ -142,18 +145,30 @@ __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float ratio
   }
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 constexpr int kAppendThreads = 256;
 constexpr int kAppendQ = 4;  // query heads whose rows are loaded together
 
-template <int D, bool FP8, int THREADS, int ITEMS>
-__global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS == 1 ? 4 : 1)
-    append_kernel(const AppendParams prm) {
+// CL: blocks of a cluster, which are a page's (e4m3; a bf16 page's blocks need not know of each other).
+template <int D, bool FP8, int THREADS, int CL>
+__global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads ? 4 : 1) append_kernel(const AppendParams prm) {
   constexpr int VPR = D / 8;
-  constexpr int ROWS = THREADS / VPR;  // tokens of a page the block takes at a time
+  constexpr int ROWS = THREADS / VPR;  // tokens of the block
   const PagedBatch& pb = prm.b;
-  const int h = blockIdx.x % pb.Hkv;
-  const int unit = blockIdx.x / pb.Hkv;
-  const int b = unit / prm.max_touched, ordinal = unit % prm.max_touched;
+  if (CL > 1) cluster_arrive();  // this block runs: the others may write to its shared memory
+  // a cluster's blocks are neighbours; otherwise the heads are, whose rows of a token lie side by side
+  unsigned rest = blockIdx.x;
+  const int fast = FP8 ? prm.subs : pb.Hkv, slow = FP8 ? pb.Hkv : prm.subs;
+  unsigned q = rest / fast;
+  const int i0 = rest - q * fast;
+  rest = q;
+  q = rest / slow;
+  const int i1 = rest - q * slow;
+  rest = q;
+  const int h = FP8 ? i1 : i0, blk = FP8 ? i0 : i1;
+  const int b = rest / static_cast<unsigned>(prm.max_touched), ordinal = rest - b * prm.max_touched;
   const SeqInfo s = load_seq(pb, b);
   const int start = s.len - s.rows;  // position of the first new row
   if (s.rows == 0) return;
@@ -166,8 +181,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS ==
   if (base >= s.len) return;
   const int page = pb.table[static_cast<size_t>(b) * pb.max_pages + block];  // checked below, with the loads under way
   const int first = max(start, base) - base, last = min(s.len, base + (1 << pb.page_shift)) - base;  // slots [first, last)
-  const int vec = threadIdx.x % VPR, slot0 = first + threadIdx.x / VPR;
-  const size_t row0 = static_cast<size_t>(s.row0 + base + slot0 - start);  // this thread's first token row
+  const int vec = threadIdx.x % VPR, slot = first + blk * ROWS + threadIdx.x / VPR;
+  const size_t row0 = static_cast<size_t>(s.row0 + base + slot - start);  // this thread's token row
   // the lane with the other halves of this lane's pairs, and whether its columns turn at all
   const int half = prm.rot / 16;
   const bool turns = vec * 8 < prm.rot, inter = prm.interleaved;
@@ -177,110 +192,104 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads && ITEMS ==
   const __nv_bfloat16* qp = prm.Q + row0 * prm.ldq + h * prm.G * D + vec * 8;
   __nv_bfloat16* qop = prm.Qo + row0 * prm.ldqo + h * prm.G * D + vec * 8;
   const int limit = prm.rot > 0 ? min(last, prm.n_pos - base) : last;  // slots behind it are not written
+  const bool live = slot < limit;
 
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 kraw[ITEMS], vraw[ITEMS], qraw[kAppendQ];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const bool live = slot0 + i * ROWS < limit;
-    kraw[i] = live ? *reinterpret_cast<const uint4*>(kp + i * ROWS * prm.ldk) : zero;
-    vraw[i] = live ? *reinterpret_cast<const uint4*>(vp + i * ROWS * prm.ldv) : zero;
-  }
-  auto angles = [&](int i) {
-    Angles a;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a.c[j] = a.s[j] = make_float2(0.0f, 0.0f);
-    if (slot0 + i * ROWS < limit && turns) a = load_angles(prm, base + slot0 + i * ROWS, vec);
-    return a;
-  };
-  auto load_q = [&](int i, int g0) {
+  const uint4 kraw = live ? *reinterpret_cast<const uint4*>(kp) : zero;
+  const uint4 vraw = live ? *reinterpret_cast<const uint4*>(vp) : zero;
+  uint4 qraw[kAppendQ];
+  auto load_q = [&](int g0) {
 #pragma unroll
     for (int g = 0; g < kAppendQ; ++g)
-      qraw[g] = slot0 + i * ROWS < limit && g0 + g < prm.G
-                    ? *reinterpret_cast<const uint4*>(qp + i * ROWS * prm.ldq + (g0 + g) * D)
-                    : zero;
+      qraw[g] = live && g0 + g < prm.G ? *reinterpret_cast<const uint4*>(qp + (g0 + g) * D) : zero;
   };
-  Angles ang = angles(0);
-  load_q(0, 0);
+  Angles ang;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) ang.c[j] = ang.s[j] = make_float2(0.0f, 0.0f);
+  if (live && turns) ang = load_angles(prm, base + slot, vec);
+  load_q(0);
   if (limit < last && threadIdx.x == 0) record(pb.status, kBadPosition);
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(pb.num_pages)) {
     record(pb.status, kBadPage);
     return;
   }
   const size_t head_at = (static_cast<size_t>(page) * pb.Hkv + h) << pb.page_shift;  // row of slot 0 in the cache
-  float ak = 0.0f, av = 0.0f;
   float ks_old = 0.0f, vs_old = 0.0f;
   if (FP8 && first > 0) {
     ks_old = prm.Ks[static_cast<size_t>(page) * pb.Hkv + h];
     vs_old = prm.Vs[static_cast<size_t>(page) * pb.Hkv + h];
   }
-  Eight kx;
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const bool live = slot0 + i * ROWS < limit;
-    if (i > 0) {
-      ang = angles(i);
-      load_q(i, 0);
-    }
-    kx = rotate8<VPR>(kraw[i], ang, other, turns, inter);
-    if constexpr (FP8) {
-      ak = amax8(kx, ak);
-      av = amax8(unpack8(vraw[i]), av);
-    } else if (live) {
-      const size_t at = (head_at + slot0 + i * ROWS) * D + vec * 8;
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Kc) + at) = pack8_bf16(kx);
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Vc) + at) = vraw[i];
-    }
+  const Eight kx = rotate8<VPR>(kraw, ang, other, turns, inter);
+  if (!FP8 && live) {
+    const size_t at = (head_at + slot) * D + vec * 8;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Kc) + at) = pack8_bf16(kx);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(prm.Vc) + at) = vraw;
+  }
+  auto queries = [&] {
     for (int g0 = 0; g0 < prm.G; g0 += kAppendQ) {
-      if (g0 > 0) load_q(i, g0);
+      if (g0 > 0) load_q(g0);
 #pragma unroll
       for (int g = 0; g < kAppendQ; ++g) {
         const uint4 y = pack8_bf16(rotate8<VPR>(qraw[g], ang, other, turns, inter));
-        if (live && g0 + g < prm.G) *reinterpret_cast<uint4*>(qop + i * ROWS * prm.ldqo + (g0 + g) * D) = y;
+        if (live && g0 + g < prm.G) *reinterpret_cast<uint4*>(qop + (g0 + g) * D) = y;
       }
     }
-  }
+  };
+  if (!FP8) queries();
   if constexpr (FP8) {
-    __shared__ float red[2][THREADS / 32];
+    float ak = amax8(kx, 0.0f), av = amax8(unpack8(vraw), 0.0f);
+    __shared__ float2 red[THREADS / 32], all[CL];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
       av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
     }
     if (THREADS > 32) {
-      if ((threadIdx.x & 31) == 0) {
-        red[0][threadIdx.x >> 5] = ak;
-        red[1][threadIdx.x >> 5] = av;
-      }
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(ak, av);
       __syncthreads();  // also: every thread has read the old scales
+      if (CL == 1 || threadIdx.x < CL) {
 #pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        ak = fmaxf(ak, red[0][w]);
-        av = fmaxf(av, red[1][w]);
+        for (int w = 0; w < THREADS / 32; ++w) {
+          ak = fmaxf(ak, red[w].x);
+          av = fmaxf(av, red[w].y);
+        }
+      }
+      if constexpr (CL > 1) {
+        // thread r leaves this block's maxima in block r's shared memory (once all blocks run); after the barrier
+        // all are local.  The queries are turned while it completes.
+        cluster_wait();
+        if (threadIdx.x < CL)
+          asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_smem(smem_u32(&all[blk]), threadIdx.x)),
+                       "f"(ak), "f"(av)
+                       : "memory");
+        cluster_arrive();
+        queries();
+        cluster_wait();
+        ak = av = 0.0f;
+#pragma unroll
+        for (int w = 0; w < CL; ++w) {
+          ak = fmaxf(ak, all[w].x);
+          av = fmaxf(av, all[w].y);
+        }
       }
     } else {
       __syncwarp();
     }
+    if (CL == 1) queries();
     const float ks = fmaxf(ks_old, needed_scale(ak)), vs = fmaxf(vs_old, needed_scale(av));
     uint8_t* kc = static_cast<uint8_t*>(prm.Kc) + head_at * D;
     uint8_t* vc = static_cast<uint8_t*>(prm.Vc) + head_at * D;
-    if (threadIdx.x == 0) {
+    const int t = blk * THREADS + threadIdx.x;
+    if (t == 0) {
       prm.Ks[static_cast<size_t>(page) * pb.Hkv + h] = ks;
       prm.Vs[static_cast<size_t>(page) * pb.Hkv + h] = vs;
     }
-    if (first > 0 && ks > ks_old) rescale_codes(kc, first * D, ks_old / ks, threadIdx.x, THREADS);
-    if (first > 0 && vs > vs_old) rescale_codes(vc, first * D, vs_old / vs, threadIdx.x, THREADS);
-    const float ki = 1.0f / ks, vi = 1.0f / vs;  // exact for the powers of two written here
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      if (ITEMS > 1) {
-        ang = angles(i);
-        kx = rotate8<VPR>(kraw[i], ang, other, turns, inter);
-      }
-      if (slot0 + i * ROWS >= limit) continue;
-      const size_t at = static_cast<size_t>(slot0 + i * ROWS) * D + vec * 8;
-      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(kx, ki);
-      *reinterpret_cast<uint2*>(vc + at) = pack8_e4m3(unpack8(vraw[i]), vi);
+    if (first > 0 && ks > ks_old) rescale_codes(kc, first * D, ks_old / ks, t, THREADS * CL);
+    if (first > 0 && vs > vs_old) rescale_codes(vc, first * D, vs_old / vs, t, THREADS * CL);
+    if (live) {
+      const size_t at = static_cast<size_t>(slot) * D + vec * 8;
+      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(kx, 1.0f / ks);  // exact for the powers of two written here
+      *reinterpret_cast<uint2*>(vc + at) = pack8_e4m3(unpack8(vraw), 1.0f / vs);
     }
   }
 }

@@ -119,19 +119,36 @@ bool make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache* c, 
   return true;
 }
 
+template <int D, bool FP8, int THREADS, int CL>
+int launch_append_blocks(fa::AppendParams prm, long long units, int subs, cudaStream_t st) {
+  prm.subs = subs;
+  if (units * subs > INT_MAX) return FA_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * subs));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CL;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fa::append_kernel<D, FP8, THREADS, CL>, prm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+// units: pages x key/value heads; most: new tokens of a sequence, at most.
 template <int D, bool FP8>
-int launch_append(const fa::AppendParams& prm, long long grid, int most, cudaStream_t st) {
+int launch_append(const fa::AppendParams& prm, long long units, int most, cudaStream_t st) {
   constexpr int N = fa::kAppendThreads, VPR = D / 8;
-  const unsigned g = static_cast<unsigned>(grid);
-  // new tokens that a page can get, by the rows a block takes at a time
-  const int rows = most < (1 << prm.b.page_shift) ? most : 1 << prm.b.page_shift;
-  const int items = (rows + N / VPR - 1) / (N / VPR);
-  if (rows <= 32 / VPR) fa::append_kernel<D, FP8, 32, 1><<<g, 32, 0, st>>>(prm);
-  else if (items <= 1) fa::append_kernel<D, FP8, N, 1><<<g, N, 0, st>>>(prm);
-  else if (items <= 2) fa::append_kernel<D, FP8, N, 2><<<g, N, 0, st>>>(prm);
-  else if (items <= 4) fa::append_kernel<D, FP8, N, 4><<<g, N, 0, st>>>(prm);
-  else fa::append_kernel<D, FP8, N, 8><<<g, N, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const int rows = most < (1 << prm.b.page_shift) ? most : 1 << prm.b.page_shift;  // new tokens that a page can get
+  if (rows <= 32 / VPR) return launch_append_blocks<D, FP8, 32, 1>(prm, units, 1, st);
+  const int subs = (rows + N / VPR - 1) / (N / VPR);
+  if (!FP8 || subs == 1) return launch_append_blocks<D, FP8, N, 1>(prm, units, subs, st);
+  if constexpr (FP8) {
+    if (subs == 2) return launch_append_blocks<D, FP8, N, 2>(prm, units, 2, st);
+    if (subs <= 4) return launch_append_blocks<D, FP8, N, 4>(prm, units, 4, st);
+    return launch_append_blocks<D, FP8, N, 8>(prm, units, 8, st);
+  }
+  return FA_ERR_CUDA;  // not reached
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -285,12 +302,11 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
   const int most = batch->max_q < T ? batch->max_q : T;
   prm.max_touched = (most + cache->page_size - 2) / cache->page_size + 1;
   if (prm.max_touched > batch->max_pages) prm.max_touched = batch->max_pages;
-  const long long grid = static_cast<long long>(batch->B) * prm.max_touched * Hkv;
-  if (grid > INT_MAX) return FA_ERR_UNSUPPORTED;
+  const long long units = static_cast<long long>(batch->B) * prm.max_touched * Hkv;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fp8 = cache->type == FA_CACHE_E4M3;
-  if (d == 128) return fp8 ? launch_append<128, true>(prm, grid, most, st) : launch_append<128, false>(prm, grid, most, st);
-  return fp8 ? launch_append<64, true>(prm, grid, most, st) : launch_append<64, false>(prm, grid, most, st);
+  if (d == 128) return fp8 ? launch_append<128, true>(prm, units, most, st) : launch_append<128, false>(prm, units, most, st);
+  return fp8 ? launch_append<64, true>(prm, units, most, st) : launch_append<64, false>(prm, units, most, st);
 }
 
 size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, int Hq) {
