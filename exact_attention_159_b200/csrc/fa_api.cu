@@ -491,7 +491,7 @@ int bwd_finish_launch(uint8_t* wsb, const WsLayout& ws, void* dQ, int BH, int Nq
 
 extern "C" {
 
-int fa_version(void) { return 100; }
+int fa_version(void) { return 101; }
 
 const char* fa_strerror(int status) {
   switch (status) {

@@ -342,7 +342,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_launch();
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled tiles need a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicCAS(prm.b.status, 0, kSiteDecode | 0x7F);
+    if (threadIdx.x == 0) {
+      atomicCAS(prm.b.status, 0, kSiteDecode | 0x7F);
+      prm.plan[blockIdx.x] = CutPlan{};
+    }
     return;
   }
   if (threadIdx.x == 0) {
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
             const int lr = 8 * n + 2 * t + e, row = rb * (8 * NT) + lr;
             if (lr >= rows) continue;
             float x[RUN];
-            const float scale = !w.whole ? 1.0f : acc.l[n][e] > 0.0f ? 1.0f / acc.l[n][e] : 0.0f;
+            const float scale = !w.whole ? 1.0f : acc.l[n][e] != 0.0f ? 1.0f / acc.l[n][e] : 0.0f;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) x[2 * j] = acc.o[n][j][e] * scale, x[2 * j + 1] = acc.o[n][j][2 + e] * scale;
             if (w.whole) {
@@ -744,8 +747,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           }
         } else if (w.whole) {
           // two rows' values of one column become two columns of one row, so that a lane stores pairs
-          const float i0 = acc.l[n][0] > 0.0f ? 1.0f / acc.l[n][0] : 0.0f;
-          const float i1 = acc.l[n][1] > 0.0f ? 1.0f / acc.l[n][1] : 0.0f;
+          const float i0 = acc.l[n][0] != 0.0f ? 1.0f / acc.l[n][0] : 0.0f;
+          const float i1 = acc.l[n][1] != 0.0f ? 1.0f / acc.l[n][1] : 0.0f;
           const int row = rb * (8 * NT) + 8 * n + gid;
           const size_t at = static_cast<size_t>(w.d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G;
 #pragma unroll
@@ -771,7 +774,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
             if (lr >= rows) continue;
             if (w.whole)
               prm.LSE[static_cast<size_t>(w.d.s.row0 + row / prm.G) * prm.Hq + h * prm.G + row % prm.G] =
-                  acc.l[n][e] > 0.0f ? (acc.m[n][e] + log2f(acc.l[n][e])) * 0.69314718055994531f : -INFINITY;
+                  acc.l[n][e] != 0.0f ? (acc.m[n][e] + log2f(acc.l[n][e])) * 0.69314718055994531f : -INFINITY;
             else
               prm.part_ml[slot + lr] = make_float2(acc.m[n][e], acc.l[n][e]);
           }

@@ -64,7 +64,8 @@ __device__ __forceinline__ void join_row(const JoinItem& it, int lr, int begin, 
   for (int c = 0; c < C; ++c) o[c] = 0.0f;
   for (int k0 = 0; k0 < n; k0 += 32) {
     const float2 ml = k0 + lane < n ? it.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.0f);
-    const float w = ml.x == -INFINITY ? 0.0f : exp2_sfu(ml.x - m);
+    // l = 0: the row sees no key of the part, whose O may not be written
+    const float w = ml.y == 0.0f ? 0.0f : exp2_sfu(ml.x - (m == -INFINITY ? 0.0f : m));
     l = fmaf(w, ml.y, l);
     const int here = min(32, n - k0);
 #pragma unroll 8
@@ -73,7 +74,7 @@ __device__ __forceinline__ void join_row(const JoinItem& it, int lr, int begin, 
       float v[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) v[c] = 0.0f;
-      if (wk > 0.0f) {  // a part in which the row sees no key may not be written
+      if (wk > 0.0f) {
         const float* p = it.part_o + at(k0 + k) * D + lane * C;
         if constexpr (C == 4) {
           const float4 x = *reinterpret_cast<const float4*>(p);
@@ -95,7 +96,7 @@ template <int D>
 __device__ __forceinline__ void join_store(const JoinItem& it, int lr, const float (&o)[D / 32], float m, float l) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31, row = it.plan.row0 + lr;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   const size_t at = static_cast<size_t>(it.plan.token0 + row / it.G) * it.Hq + it.plan.h * it.G + row % it.G;
   uint32_t* to = reinterpret_cast<uint32_t*>(it.O + at * D + lane * C);
   if constexpr (C == 4) {
@@ -103,7 +104,7 @@ __device__ __forceinline__ void join_store(const JoinItem& it, int lr, const flo
   } else {
     *to = pack_bf16x2(o[0] * inv, o[1] * inv);
   }
-  if (lane == 0) it.LSE[at] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0) it.LSE[at] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Blocks 0 .. (n_dec - 1) * dec.rows - 1: the cuts of decode_kernel's n_dec shares, a block a row; after them

@@ -159,8 +159,10 @@ FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   d.half = d.pairs > 0 && rows - static_cast<long long>(d.pairs - 1) * kPreRows <= kTile;
   // pair p's last row (when the pair is full) is token (256 (p + 1) - 1) / G, which sees keys up to len - rows +
   // that; a tile has 128 keys, and 256 p is a multiple of 128, which leaves (x + 2 p) / G
-  d.linear = p.causal && d.s.len >= d.s.rows;
-  d.x = d.linear ? static_cast<int>((static_cast<long long>(d.s.len - d.s.rows) * p.G + 255) / 128) : 0;
+  // (groups so wide and sequences so long that x would not fit count every tile for every pair)
+  const long long x = (static_cast<long long>(d.s.len - d.s.rows) * p.G + 255) / 128;
+  d.linear = p.causal && d.s.len >= d.s.rows && x < (1 << 30);
+  d.x = d.linear ? static_cast<int>(x) : 0;
   return d;
 }
 FA_HD long long prefill_per(long long total) {
@@ -339,7 +341,10 @@ __global__ void __launch_bounds__(384, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   grid_dependency_launch();
   if ((smem_u32(smem) & 1023u) != 0) {  // swizzled tiles need a 1024-byte aligned base
-    if (threadIdx.x == 0) atomicCAS(prm.b.status, 0, kSitePrefill | 0x7F);
+    if (threadIdx.x == 0) {
+      atomicCAS(prm.b.status, 0, kSitePrefill | 0x7F);
+      prm.plan[blockIdx.x] = CutPlan{};
+    }
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -964,7 +969,7 @@ __global__ void __launch_bounds__(384, 1)
       const size_t slot = static_cast<size_t>(decode_slot(blockIdx.x, w->step0)) * kPreRows + (split ? 0 : t * kTile) + r;
       if (end > t0 && stores) {
         tc_fence_after();
-        const float scale = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        const float scale = !whole ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
         // rows of W bytes through the tile's part of Q, which no MMA reads any more: results in one go, parts
         // (fp32, twice as wide) in two
         constexpr int W = 2 * D;
@@ -1013,8 +1018,8 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(prm.O + at * D)[i] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (real && stores) {
-        if (whole) prm.LSE[at] = l > 0.0f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        else prm.part_ml[slot] = make_float2(m_ref, l);  // m = -inf: the join takes nothing from this part
+        if (whole) prm.LSE[at] = l != 0.0f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        else prm.part_ml[slot] = make_float2(m_ref, l);  // l = 0: the join takes nothing from this part
       }
       kt0 += max(w->end[0], w->end[1]) - t0;
       __syncwarp();

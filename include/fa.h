@@ -309,7 +309,7 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
  * shorter than its new tokens) gets O = 0, LSE = -inf.  Slots behind a
  * sequence's end may hold anything, NaN included.  Keys and values of live
  * tokens, queries and scales must be finite: one that is not may reach every
- * row of its sequence.  For an e4m3 cache any scales >= 0 serve (value scales
+ * row of its sequence (as NaN).  For an e4m3 cache any scales >= 0 serve (value scales
  * below 2^-100 count as 2^-100, and they should not exceed 2^60).
  *
  * Where a sequence's keys are cut for the GPU's SMs depends on the lengths of

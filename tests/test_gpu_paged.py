@@ -182,6 +182,67 @@ def test_rows_behind_the_batch_and_strided_queries(e4m3, q_lens):
     assert bool((out[bt.T_live:] == 7).all()) and bool((lse[bt.T_live:] == 7).all())
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [33, 64, 128])
+def test_wide_groups(e4m3, G):
+    """Multi-query attention: single tokens whose query heads alone are more rows than a decode item holds."""
+    bt = Batch([1, 1, 3], [700, 45, 130], G, 1, 64, 32, e4m3, seed=33)
+    out, lse, scale = attend(bt)
+    check(bt, out, lse, scale, True, f"G {G} e4m3={e4m3}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("q_lens", [[1, 1], [200, 30]])
+def test_cache_beyond_32_bit_offsets(e4m3, q_lens):
+    """Pages whose bytes (and elements) lie beyond 2^32 of the pool: attention, and appends to them."""
+    bt = Batch(q_lens, [260, 100], 8, 8, 128, 128, e4m3, seed=34, dead=None)
+    n = 2 ** 32 // (8 * 128 * 128) + 40
+    far = n - 1 - torch.arange(bt.n_pages)  # the small pool's pages at the large one's end
+    big = []
+    for x in (bt.k, bt.v):
+        y = torch.empty((n, 8, 128, 128), dtype=x.dtype, device="cuda")
+        y[far.cuda()] = x.cuda()
+        big.append(y)
+    scales = [None, None]
+    if e4m3:
+        for i, x in enumerate((bt.ks, bt.vs)):
+            scales[i] = torch.zeros((n, 8), device="cuda")
+            scales[i][far.cuda()] = x.cuda()
+    cache = api.PagedCache(*big, *scales)
+    table = torch.where(bt.table >= 0, n - 1 - bt.table, bt.table)
+    batch = api.PagedBatch(table.cuda(), bt.cu_q.cuda(), torch.tensor(bt.lens, dtype=torch.int32).cuda(), max(q_lens))
+    out, lse = api.fa_fwd_paged(bt.q.cuda(), cache, batch, 0.1)
+    assert _status() == (0, 0)
+    check(bt, out, lse, 0.1, True, f"far pages e4m3={e4m3}")
+    small, sb, _ = bt.dev()
+    k, v = (torch.randn(bt.T, 8, 128, device="cuda").bfloat16() for _ in range(2))
+    api.fa_cache_append(k, v, cache, batch)
+    api.fa_cache_append(k, v, small, sb)
+    assert _status() == (0, 0)
+    bits = torch.uint8 if e4m3 else torch.int16
+    for y, x in zip(big, (bt.dk, bt.dv)):
+        assert torch.equal(y[far.cuda()].view(bits), x.view(bits))
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [200, 40]])
+def test_nan_in_a_live_key_or_value_shows(q_lens):
+    """It reaches rows of its own sequence as NaN, in O and LSE, and no other sequence's."""
+    for which in ("k", "v"):
+        for e4m3 in (False, True):
+            bt = Batch(q_lens, [300, 4000], 8, 2, 128, 32, e4m3, seed=35)
+            x = getattr(bt, which)
+            bits = torch.uint8 if e4m3 else torch.int16
+            x[int(bt.table[1, 60])].view(bits)[:, 7, 3] = torch.tensor([float("nan")]).to(x.dtype).view(bits)
+            out, lse, scale = attend(bt)
+            first = slice(0, q_lens[0])
+            O, L, tO, tL = reference(bt, scale, True)
+            assert bool(((out[first].double().cpu() - O[first]).abs() <= tO[first]).all())
+            assert bool(((lse[first].double().cpu() - L[first]).abs() <= tL[first]).all())
+            assert bool(out[q_lens[0]:].isnan().any())
+            if which == "k":
+                assert bool(lse[q_lens[0]:].isnan().all()) and bool(out[q_lens[0]:].isnan().all())
+
+
 def test_empty_calls_launch_nothing():
     bt = Batch([1], [5], 4, 2, 64, 16, False, seed=1)
     cache, batch, q = bt.dev()
@@ -520,6 +581,41 @@ def test_captured_step_replays_with_new_lengths(e4m3):
             bt.ks, bt.vs = bt.dks.cpu(), bt.dvs.cpu()
         bt.q = qr.cpu()
         check(bt, out, lse, 0.1, True, f"replay {n}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_captured_prompt_chunk(e4m3):
+    """Prompt chunks (appends by clusters of blocks, both attention kernels and the join) in a captured graph."""
+    bt = Batch([200, 1, 33], [330, 90, 33], 8, 2, 128, 128, e4m3, seed=52, dead=None)
+    cache, batch, q = bt.dev()
+    k, v = (torch.randn(bt.T, 2, 128, device="cuda").bfloat16() for _ in range(2))
+    cos, sin = torch.ones(512, 64, device="cuda"), torch.zeros(512, 64, device="cuda")
+    out, lse, qr = torch.zeros_like(q), torch.zeros(bt.T, 8, device="cuda"), torch.zeros_like(q)
+    ws = torch.empty(api.fa_fwd_paged_workspace_size(cache, batch, bt.T, 8), dtype=torch.uint8, device="cuda")
+
+    def step():
+        api.fa_cache_append(k, v, cache, batch, cos=cos, sin=sin, q=q, q_out=qr)
+        api.fa_fwd_paged(qr, cache, batch, 0.1, True, out=out, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x in (q, k, v):
+        x.copy_(torch.randn(x.shape, device="cuda"))
+    for n in range(3):
+        ws.fill_(0xFF)
+        out.zero_()
+        graph.replay()
+        assert _status() == (0, 0)
+        bt.k, bt.v, bt.q = bt.dk.cpu(), bt.dv.cpu(), qr.cpu()
+        if e4m3:
+            bt.ks, bt.vs = bt.dks.cpu(), bt.dvs.cpu()
+        check(bt, out, lse, 0.1, True, f"chunk replay {n} e4m3={e4m3}")
 
 
 @pytest.mark.parametrize("q_lens", [[1, 1, 1], [150, 1, 9]])
