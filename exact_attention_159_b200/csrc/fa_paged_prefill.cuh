@@ -459,6 +459,16 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive(&seg_full[si]);
         }
         if (!more) break;
+        // the segment's rows of Q on their way to L2: they are read when the segment before has ended
+        for (int r = lane; r < kPreRows; r += 32) {
+          const int row = w.p * kPreRows + r, token = row / prm.G;
+          if (token >= w.d.s.rows) break;
+          const __nv_bfloat16* q =
+              prm.Q + static_cast<size_t>(w.d.s.row0 + token) * prm.ldq + (w.h * prm.G + row % prm.G) * D;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+        }
+        __syncwarp();
         for (int j = w.first(); j < end && ok; ++j, ++kt) {
           const int keys = min(kTile, w.d.s.len - j * kTile);
           const int boxes = (keys + box_rows - 1) >> shift;
@@ -737,53 +747,65 @@ __global__ void __launch_bounds__(384, 1)
       if (end > t0) {
         // the tile's last S is done, since these threads have seen its scores
         const __nv_bfloat16* mine = prm.Q + (real ? static_cast<size_t>(w->row0 + token) * prm.ldq + head * D : 0);
-        uint4 x[LPR];
+        // four rows at a time, the next four on their way: unrolled over all rows the code, run once a segment,
+        // took longer to fetch than to run
+        uint4 x[4], ahead[4];
+        auto load = [&](uint4(&y)[4], int i0) {
 #pragma unroll
-        for (int i = 0; i < LPR; ++i) {
-          const int from = i * RPI + sub;
-          const auto* q = reinterpret_cast<const __nv_bfloat16*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
-          x[i] = (reals >> from) & 1 ? __ldg(reinterpret_cast<const uint4*>(q) + chunk) : make_uint4(0u, 0u, 0u, 0u);
-        }
+          for (int k = 0; k < 4; ++k) {
+            const int from = (i0 + k) * RPI + sub;
+            const auto* q = reinterpret_cast<const __nv_bfloat16*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
+            y[k] = (reals >> from) & 1 ? __ldg(reinterpret_cast<const uint4*>(q) + chunk) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        };
+        load(ahead, 0);
+#pragma unroll 1
+        for (int i0 = 0; i0 < LPR; i0 += 4) {
 #pragma unroll
-        for (int i = 0; i < LPR; ++i) {
-          const int row = quarter * 32 + i * RPI + sub;  // of the tile
-          uint8_t* to = smem + L::kQ + t * L::kQBytes;
-          if constexpr (FP8) {
-            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float f[8], amax = 0.0f;
+          for (int k = 0; k < 4; ++k) x[k] = ahead[k];
+          if (i0 + 4 < LPR) load(ahead, i0 + 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = __uint_as_float(v[k] << 16);
-              f[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u);
-              amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int i = i0 + k4;
+            const int row = quarter * 32 + i * RPI + sub;  // of the tile
+            uint8_t* to = smem + L::kQ + t * L::kQBytes;
+            if constexpr (FP8) {
+              const uint32_t v[4] = {x[k4].x, x[k4].y, x[k4].z, x[k4].w};
+              float f[8], amax = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                f[2 * k] = __uint_as_float(v[k] << 16);
+                f[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u);
+                amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+              }
+#pragma unroll
+              for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+              // q * 256 / (a power of two above the row's largest magnitude) = first part + second part, both e4m3
+              const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 255);
+              const float down = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
+              const int e_row = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);  // for the row's own thread
+              if (i == lane / RPI) sl2 = prm.scale_log2 * __uint_as_float(static_cast<uint32_t>(e_row - 8) << 23);
+              uint32_t part[2][2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) f[4 * k + n] *= down;
+                part[0][k] = e4m3x2(f[4 * k], f[4 * k + 1]) | (e4m3x2(f[4 * k + 2], f[4 * k + 3]) << 16);
+                uint32_t h0, h1;
+                halves_of_e4m3(part[0][k], h0, h1);
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+                part[1][k] = e4m3x2(f[4 * k] - a.x, f[4 * k + 1] - a.y) |
+                             (e4m3x2(f[4 * k + 2] - b.x, f[4 * k + 3] - b.y) << 16);
+              }
+              const int c = chunk >> 1;  // 16 bytes are two lanes' eight codes
+              to += (D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4)) + (chunk & 1) * 8;
+              *reinterpret_cast<uint2*>(to) = make_uint2(part[0][0], part[0][1]);
+              *reinterpret_cast<uint2*>(to + kTile * D) = make_uint2(part[1][0], part[1][1]);
+            } else {
+              *reinterpret_cast<uint4*>(to + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = x[k4];
             }
-#pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // q * 256 / (a power of two above the row's largest magnitude) = first part + second part, both e4m3
-            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) + 1, 8), 255);
-            const float down = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
-            const int e_row = __shfl_sync(0xffffffffu, e, (lane % RPI) * LPR);  // for the row's own thread
-            if (i == lane / RPI) sl2 = prm.scale_log2 * __uint_as_float(static_cast<uint32_t>(e_row - 8) << 23);
-            uint32_t part[2][2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-              for (int n = 0; n < 4; ++n) f[4 * k + n] *= down;
-              part[0][k] = e4m3x2(f[4 * k], f[4 * k + 1]) | (e4m3x2(f[4 * k + 2], f[4 * k + 3]) << 16);
-              uint32_t h0, h1;
-              halves_of_e4m3(part[0][k], h0, h1);
-              const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-              const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-              part[1][k] = e4m3x2(f[4 * k] - a.x, f[4 * k + 1] - a.y) |
-                           (e4m3x2(f[4 * k + 2] - b.x, f[4 * k + 3] - b.y) << 16);
-            }
-            const int c = chunk >> 1;  // 16 bytes are two lanes' eight codes
-            to += (D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4)) + (chunk & 1) * 8;
-            *reinterpret_cast<uint2*>(to) = make_uint2(part[0][0], part[0][1]);
-            *reinterpret_cast<uint2*>(to + kTile * D) = make_uint2(part[1][0], part[1][1]);
-          } else {
-            *reinterpret_cast<uint4*>(to + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = x[i];
           }
         }
         fence_proxy_async();
@@ -970,15 +992,20 @@ __global__ void __launch_bounds__(384, 1)
       if (end > t0 && stores) {
         tc_fence_after();
         const float scale = !whole ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
-        // rows of W bytes through the tile's part of Q, which no MMA reads any more: results in one go, parts
-        // (fp32, twice as wide) in two
-        constexpr int W = 2 * D;
-        uint8_t* stage = smem + L::kQ + t * L::kQBytes + quarter * (32 * W);
+        // rows of W bytes (results in one go, parts, fp32 and twice as wide, in two) through the shared memory that
+        // held these same rows of Q: no MMA reads them any more, and no other warp writes there when it goes on
+        // to the next segment's
+        constexpr int W = 2 * D, RB = FP8 ? D : 128;  // a row of Q: RB bytes in each of W / RB parts
+        auto stage = [&](int lr, int k) {
+          const int part = k / (RB / 16), kk = k % (RB / 16), x = RB == 128 ? lr & 7 : (lr >> 1) & 3;
+          return reinterpret_cast<uint4*>(smem + L::kQ + t * L::kQBytes + part * (kTile * RB) + (quarter * 32 + lr) * RB +
+                                          ((kk ^ x) << 4));
+        };
         const auto mine = reinterpret_cast<unsigned long long>(whole ? static_cast<void*>(prm.O + at * D)
                                                                      : static_cast<void*>(prm.part_o + slot * D));
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
             uint32_t o[32];
             tmem_ld32(tO + (D / 2) * half + 32 * c, o);
@@ -992,22 +1019,21 @@ __global__ void __launch_bounds__(384, 1)
                 for (int k = 0; k < 4; ++k)
                   v[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * scale, __uint_as_float(o[8 * i + 2 * k + 1]) * scale);
                 const int k = (D / 16) * half + 4 * c + i;
-                *reinterpret_cast<uint4*>(stage + lane * W + ((k ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                *stage(lane, k) = make_uint4(v[0], v[1], v[2], v[3]);
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(stage + lane * W + (((8 * c + i) ^ (lane & 7)) << 4)) =
-                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                *stage(lane, 8 * c + i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
           if (whole && half == 0) continue;
           __syncwarp();
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < LPR; ++i) {
             const int from = i * RPI + sub;
             auto* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, from));
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + from * W + ((chunk ^ (from & 7)) << 4));
+            const uint4 v = *stage(from, chunk);
             if ((reals >> from) & 1) *reinterpret_cast<uint4*>(to + (whole ? 0 : half * W) + chunk * 16) = v;
           }
           __syncwarp();
