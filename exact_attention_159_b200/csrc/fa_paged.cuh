@@ -14,6 +14,8 @@
 
 #include "sm100.cuh"
 
+#define FA_HD __host__ __device__ __forceinline__
+
 namespace fa {
 
 enum : int {
@@ -29,6 +31,11 @@ __device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddep
 // Waits for the kernel before, if this one was launched to overlap with it, to end, its writes visible.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// a / b, of 32 bits where both are (64-bit divisions are a long dependent sequence at every CTA's start).
+FA_HD long long divide(long long a, long long b) {
+  return ((a | b) >> 31) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 struct PagedBatch {
   const int* table;  // [B, max_pages]
   const int* cu_q;   // [B + 1]
@@ -41,8 +48,6 @@ struct PagedBatch {
 struct SeqInfo {
   int row0, rows, len;  // first token row, new rows, tokens in all
 };
-
-#define FA_HD __host__ __device__ __forceinline__
 
 FA_HD void record(int* status, int what) {
 #ifdef __CUDA_ARCH__

@@ -27,11 +27,13 @@ constexpr int kWholeKeys = 512, kWholeItems = 64;
 
 // Sequences of at most this many rows (new tokens x query heads of a key/value head) go to the kernel of few
 // rows, longer ones to the tensor-core tiles, whose time hardly depends on the rows up to 128.  24 sequences
-// of 4096 keys, 8 x 4 heads, and one of 65536, few rows against tiles: e4m3 at 32 rows 91 / 117 us and 72 / 79
-// us, at 48 rows 119 / 117 us and 93 / 81 us; bf16 at 16 rows 81 / 100 us and 59 / 79 us, at 24 rows 94 / 101 us
-// and 98 / 80 us.
+// of 4096 keys, 8 x 4 heads, and one of 65536, few rows against tiles: e4m3 at 32 rows 92 / 98 us and 67 / 74
+// us, at 48 rows 119 / 98 us and 86 / 74 us; bf16 at 16 rows 83 / 99 us and 59 / 79 us, at 24 rows 94 / 101 us
+// and 99 / 80 us.
 constexpr int kDecodeMaxRowsBf16 = 16, kDecodeMaxRowsE4m3 = 32;
-int decode_max_rows(const fa_paged_cache* c) { return c->type == FA_CACHE_E4M3 ? kDecodeMaxRowsE4m3 : kDecodeMaxRowsBf16; }
+int decode_max_rows(const fa_paged_cache* c) {
+  return c->type == FA_CACHE_E4M3 ? kDecodeMaxRowsE4m3 : kDecodeMaxRowsBf16;
+}
 
 struct Sizes {
   size_t cache, scales, table;

@@ -39,7 +39,7 @@ namespace fa {
 constexpr int kSiteDecode = 0xD00;
 constexpr int kDecRows = 16;       // most query rows of an item
 constexpr int kDecCtas = 2 * 148;  // two on each SM
-constexpr int kDecThreads = 160;   // four consumer warps, one producer warp
+constexpr int kDecThreads = 192;   // four consumer warps, a producer warp for K and one for V
 constexpr int kDecStageBytes = 98304;
 constexpr int kDecMinTiles = 2;    // a CTA's share is at least this many tiles
 constexpr int kDecItemCost = 1;    // tiles' worth of time that starting and ending an item takes
@@ -73,7 +73,7 @@ struct Cut {
 };
 FA_HD Cut cut_of(long long per, int c, int tile, int n) {
   const long long begin = per * c - tile;
-  return Cut{static_cast<int>(begin / per), static_cast<int>((begin + n - 1) / per)};
+  return Cut{static_cast<int>(divide(begin, per)), static_cast<int>(divide(begin + n - 1, per))};
 }
 
 struct DecodeParams {
@@ -129,7 +129,7 @@ FA_HD long long decode_units(const DecodeParams& p, const DecodeSeq& d) {
   return static_cast<long long>(d.items) * (p.whole ? 1 : d.tiles + kDecItemCost);
 }
 FA_HD long long decode_per(const DecodeParams& p, long long total, int n_cta) {
-  const long long per = (total + n_cta - 1) / n_cta;
+  const long long per = divide(total + n_cta - 1, n_cta);
   return !p.whole && per < kDecMinTiles + kDecItemCost ? kDecMinTiles + kDecItemCost : per;
 }
 
@@ -202,8 +202,8 @@ struct DecodeWalk {
     b = s.b;
     d = decode_seq(p, b);
     const int units = d.tiles + kDecItemCost;
-    item = static_cast<int>(p.whole ? s.off : s.off / units);
-    u0 = p.whole ? 0 : static_cast<int>(s.off % units);
+    item = static_cast<int>(p.whole ? s.off : divide(s.off, units));
+    u0 = p.whole ? 0 : static_cast<int>(s.off - static_cast<long long>(item) * units);
     cut(p);
     return t1 > 0 || next(p);
   }
@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4);
+      mbar_init(&full[i], 2);   // both producers
+      mbar_init(&empty[i], 4);  // the consumer warps
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -372,11 +372,14 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int box_shift = min(prm.b.page_shift, FP8 ? 7 : 6), box_rows = 1 << box_shift;
   int it = 0;  // tiles since the start: stage it % S
 
-  if (warp == 4) {
-    // ------------------------------------------------------------------------------- producer
+  if (warp >= 4) {
+    // ------------------------------------------------------------------ producers: K (with the scales), V
+    // A lane issues the boxes of one page; an issue takes about 95 clocks, which for pages of 16 bf16 slots is
+    // 0.8 us a tile from one warp (half from two).
+    const bool is_v = warp == 5;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
     bool ok = true;
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
+    prefetch_tmap(map);
     do {
       const int h = w.item % prm.b.Hkv;
       const int n_pages = (w.d.s.len + (1 << prm.b.page_shift) - 1) >> prm.b.page_shift;
@@ -395,14 +398,14 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           held = first_page >> 5;
           const int i = held * 32 + lane;
           page = i < n_pages ? load_page(prm.b, w.b, i) : -1;
-          if (FP8 && page >= 0) {
+          if (FP8 && !is_v && page >= 0) {
             const size_t at = static_cast<size_t>(page) * prm.b.Hkv + h;
             sc = page_scales(prm.Ks[at], prm.Vs[at]);
           }
         }
         const int my_page = __shfl_sync(0xffffffffu, page, (first_page + lane) & 31);
         float4 my_sc = sc;
-        if constexpr (FP8) {
+        if (FP8 && !is_v) {
           my_sc.x = __shfl_sync(0xffffffffu, sc.x, (first_page + lane) & 31);
           my_sc.y = __shfl_sync(0xffffffffu, sc.y, (first_page + lane) & 31);
           my_sc.z = __shfl_sync(0xffffffffu, sc.z, (first_page + lane) & 31);
@@ -410,21 +413,18 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         }
         const int st = it % S;
         if (!(ok = wait_warp(&empty[st], ((it / S) & 1) ^ 1, g, kSiteDecode | 1))) break;
-        if (FP8 && lane < boxes) meta[st * L::kBoxes + lane] = my_sc;
+        if (FP8 && !is_v && lane < boxes) meta[st * L::kBoxes + lane] = my_sc;
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(&full[st], 2 * boxes * box_rows * L::kRowBytes);
+        if (lane == 0) mbar_expect_tx(&full[st], boxes * box_rows * L::kRowBytes);
         __syncwarp();
         if (lane < boxes) {
           // a page out of range reads as zeros beyond the map's last head
           const int z = my_page >= 0 ? my_page * prm.b.Hkv + h : prm.b.num_pages * prm.b.Hkv;
           const int y = (tile * TILE) & ((1 << prm.b.page_shift) - 1);
           constexpr int kCols = FP8 ? D : 64;
+          uint8_t* to = smem + (is_v ? L::kV : 0) + st * L::kTileBytes + lane * box_rows * (kCols * (FP8 ? 1 : 2));
 #pragma unroll
-          for (int c = 0; c < D / kCols; ++c) {
-            const int at = st * L::kTileBytes + c * L::kHalf + lane * box_rows * (kCols * (FP8 ? 1 : 2));
-            tma_load_3d(smem + at, &tmK, c * kCols, y, z, &full[st]);
-            tma_load_3d(smem + L::kV + at, &tmV, c * kCols, y, z, &full[st]);
-          }
+          for (int c = 0; c < D / kCols; ++c) tma_load_3d(to + c * L::kHalf, map, c * kCols, y, z, &full[st]);
         }
       }
     } while (ok && w.next(prm));

@@ -166,7 +166,7 @@ FA_HD PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   return d;
 }
 FA_HD long long prefill_per(long long total) {
-  const long long per = (total + kPreCtas - 1) / kPreCtas;
+  const long long per = divide(total + kPreCtas - 1, kPreCtas);
   return per < kPreMinTiles + kPreItemCost ? kPreMinTiles + kPreItemCost : per;
 }
 // Unit `off` of a sequence: head, pair and unit of the item.
@@ -177,7 +177,7 @@ template <typename F>
 FA_HD PrefillAt prefill_at(const PrefillSeq& d, long long off, const F& find) {
   PrefillAt a;
   const long long head = d.head_units();
-  a.h = static_cast<int>(off / head);
+  a.h = static_cast<int>(divide(off, head));
   const long long r = off - a.h * head;
   a.p = find(d, r);
   a.unit = static_cast<int>(r - d.before(a.p));
