@@ -41,7 +41,7 @@ constexpr int kDecRows = 16;       // most query rows of an item
 constexpr int kDecCtas = 2 * 148;  // two on each SM
 constexpr int kDecThreads = 192;   // four consumer warps, a producer warp for K and one for V
 constexpr int kDecStageBytes = 98304;
-constexpr int kDecMinTiles = 2;    // a CTA's share is at least this many tiles
+constexpr int kDecMinUnits = 2;    // a CTA's share is at least this many
 constexpr int kDecItemCost = 1;    // tiles' worth of time that starting and ending an item takes
 constexpr float kDecTau = 8.0f;    // log2 units
 constexpr float kScaleFloor = 7.8886090522101181e-31f;  // 2^-100: smaller value scales count as this
@@ -130,7 +130,7 @@ FA_HD long long decode_units(const DecodeParams& p, const DecodeSeq& d) {
 }
 FA_HD long long decode_per(const DecodeParams& p, long long total, int n_cta) {
   const long long per = divide(total + n_cta - 1, n_cta);
-  return !p.whole && per < kDecMinTiles + kDecItemCost ? kDecMinTiles + kDecItemCost : per;
+  return !p.whole && per < kDecMinUnits ? kDecMinUnits : per;
 }
 
 struct DecodeShare {
