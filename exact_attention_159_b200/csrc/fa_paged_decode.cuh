@@ -29,6 +29,8 @@
 // row holds its k indices of four MMAs, and a lane's 16-byte chunk of a value row holds its rows of eight
 // output tiles.  Keys 0..7 of an octet go to rows 0,2,4,6,1,3,5,7, which with TMA's 128-byte swizzle puts
 // the eight lanes of a load phase on eight different chunks.
+// Measured: 64 sequences of 200 to 8192 e4m3 tokens, 32 over 8 heads (555 MB), 90 to 97 us (5.8 to 6.1 of 6.56
+// TB/s measured copy); query rows on the MMA's rows instead took 114 us, one CTA an SM 260 us.
 #pragma once
 
 #include "exp2_poly.cuh"
