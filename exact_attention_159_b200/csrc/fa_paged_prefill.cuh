@@ -20,9 +20,10 @@
 //     K.  V's codes land in a staging ring and two warps turn them into halves (exact).  The scales stay outside
 //     the products: K's multiplies the scores of its 16 columns or more, V's joins the exponent (w = 2^(s +
 //     log2 vs - m), O = sum w * code, the softmax's sum is sum w / vs).  P is rounded to half.
-// Measured: 2048 tokens over 16384 keys, 32 over 8 heads (515 GFLOP): bf16 495 us at the 1.58 GHz that the power
-// cap leaves (3750 cycles per pair of tiles and key tile, the contiguous forward's rate; tensor pipe 54 %
-// active), e4m3 514 to 536 us; with K converted to halves as V is, the e4m3 kernel took 757 us.
+// Measured: 2048 tokens over 16384 keys, 32 over 8 heads (515 GFLOP): bf16 473 us at 1.955 GHz in
+// short runs, 528 us at the 1.75 GHz that the power cap leaves a loop of seconds (925 K cycles either way, 4420
+// per pair of tiles and key tile; the contiguous forward takes 928 K; tensor pipe 54 % active), e4m3 514 to 536
+// us.  An earlier form of the e4m3 kernel, which converted K to halves as it does V, took 757 us.
 #pragma once
 
 #include "exp2_poly.cuh"
