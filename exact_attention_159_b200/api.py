@@ -273,11 +273,11 @@ class PagedBatch:
         if block_table.dim() != 2:
             raise ValueError("block_table: expected [B, max_pages]")
         B, max_pages = (int(x) for x in block_table.shape)
+        if not 0 <= int(max_q) < 1 << 31:
+            raise ValueError("max_q must not be negative, and fit 32 bits")
         _need(block_table, "block_table", torch.int32, (B, max_pages))
         _need(cu_q, "cu_q", torch.int32, (B + 1,))
         _need(seq_lens, "seq_lens", torch.int32, (B,))
-        if int(max_q) < 0:
-            raise ValueError("max_q must not be negative")
         self.block_table, self.cu_q, self.seq_lens = block_table, cu_q, seq_lens
         self.B, self.max_pages, self.max_q = B, max_pages, int(max_q)
         self.device = block_table.device

@@ -57,7 +57,8 @@ int check_paged(const fa_paged_cache* c, const fa_paged_batch* b, int T, int Hq,
   if (c->type == FA_CACHE_E4M3 && (!c->K_scale || !c->V_scale)) return FA_ERR_INVALID_ARG;
   if (c->num_pages == 0 || b->max_pages == 0) return FA_ERR_INVALID_ARG;
   if (!aligned16(c->K) || !aligned16(c->V)) return FA_ERR_ALIGNMENT;
-  // int lengths and tensor-map extents stay in range
+  // int lengths, offsets within a row and tensor-map extents stay in range
+  if (static_cast<long long>(queries && Hq > c->heads ? Hq : c->heads) * c->d > INT_MAX) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->num_pages) * c->heads > INT_MAX / 2) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(b->max_pages) * c->page_size > INT_MAX / 2) return FA_ERR_UNSUPPORTED;
   z->cache = static_cast<size_t>(c->num_pages) * c->heads * c->page_size * c->d * (c->type == FA_CACHE_BF16 ? 2 : 1);
@@ -72,12 +73,24 @@ bool meets(const void* p, size_t n, const fa_paged_cache* c, const fa_paged_batc
   if (overlaps(p, n, c->K, z.cache) || overlaps(p, n, c->V, z.cache)) return true;
   if (c->type == FA_CACHE_E4M3 && (overlaps(p, n, c->K_scale, z.scales) || overlaps(p, n, c->V_scale, z.scales)))
     return true;
-  return overlaps(p, n, b->block_table, z.table) || overlaps(p, n, b->cu_q, static_cast<size_t>(b->B + 1) * 4) ||
+  return overlaps(p, n, b->block_table, z.table) || overlaps(p, n, b->cu_q, (static_cast<size_t>(b->B) + 1) * 4) ||
          overlaps(p, n, b->seq_lens, static_cast<size_t>(b->B) * 4);
 }
 
 size_t rows_bytes(int T, int64_t ld, int heads, int d) {
   return (static_cast<size_t>(T - 1) * ld + static_cast<size_t>(heads) * d) * 2;
+}
+
+// Whether T rows of `na` elements, lda apart, may share an element with T rows of `nb`, ldb apart: of equal
+// strides (a fused projection's slices) those that lie side by side within a row do not.
+bool rows_meet(const void* a, int64_t lda, int64_t na, const void* b, int64_t ldb, int64_t nb, int T) {
+  const size_t sa = (static_cast<size_t>(T - 1) * lda + na) * 2, sb = (static_cast<size_t>(T - 1) * ldb + nb) * 2;
+  if (!overlaps(a, sa, b, sb)) return false;
+  if (lda != ldb) return true;
+  const int64_t apart = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b)) -
+                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(a))) / 2 % lda;  // both 16-byte aligned
+  const int64_t off = apart < 0 ? apart + lda : apart;
+  return off < na || off + nb > lda;
 }
 
 int shift_of(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
@@ -272,6 +285,9 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
     const size_t qb = rows_bytes(T, ldq, Hq, d), ob = rows_bytes(T, ldqo, Hq, d);
     if (meets(Q, qb, cache, batch, z) || meets(Q_out, ob, cache, batch, z)) return FA_ERR_INVALID_ARG;
     // in place the rows of a fused projection lie between K's and V's, and only Q's own elements are written
+    if (Q_out == Q && ldqo == ldq &&
+        (rows_meet(Q, ldq, q_row, K, ldk, kv_row, T) || rows_meet(Q, ldq, q_row, V, ldv, kv_row, T)))
+      return FA_ERR_INVALID_ARG;
     if (!(Q_out == Q && ldqo == ldq) &&
         (overlaps(Q_out, ob, Q, qb) || overlaps(Q_out, ob, K, kb) || overlaps(Q_out, ob, V, vb)))
       return FA_ERR_INVALID_ARG;

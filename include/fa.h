@@ -291,8 +291,9 @@ typedef struct {
  *
  * A page that one call writes must belong to one sequence (and once to it):
  * two sequences that share pages may share full ones only.  Q_out may not
- * overlap the cache or, unless in place, Q; nor the cache any input.  One
- * launch.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
+ * overlap the cache or, unless in place, Q, K or V; in place, Q's rows may lie
+ * side by side with K's and V's at one stride, but share no element with them.
+ * The cache may not overlap any input.  One launch.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
  */
 int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, const void* K, int64_t ldk,
                     const void* V, int64_t ldv, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo, int Hq,

@@ -130,3 +130,45 @@ def test_plans_on_the_host(tmp_path):
     done = subprocess.run([exe], capture_output=True, text=True)
     assert done.returncode == 0, done.stdout + done.stderr
     assert "ok" in done.stdout
+
+
+# ------------------------------------------------ rows turned in place, and what 32 bits of a row cannot hold
+QKV = 4 * 64 + 2 * 2 * 64  # a fused projection's row: 4 query heads, 2 of keys, 2 of values, d = 64
+
+
+def in_place(q=0, k=256, v=384, ldk=QKV, ldv=QKV):
+    return dict(Q_ARGS, Q=A[9] + 2 * q, Qo=A[9] + 2 * q, ldq=QKV, ldqo=QKV, K=A[9] + 2 * k, ldk=ldk, V=A[9] + 2 * v,
+                ldv=ldv)
+
+
+@pytest.mark.parametrize("bad", [
+    in_place(k=0), in_place(k=248), in_place(v=128), in_place(q=128, k=64, v=384), in_place(k=QKV - 64),
+    in_place(k=256 + QKV * 3, v=QKV * 2 + 200), in_place(ldk=2 * QKV), in_place(ldv=1024),
+])
+def test_keys_and_values_among_queries_turned_in_place_are_refused(lib, bad):
+    """Rows of K or V that share elements with the queries written in place (or are laid out so that they may)."""
+    assert append(lib, **bad) == INVALID
+
+
+@pytest.mark.parametrize("good", [in_place(), in_place(q=256, k=0, v=128), in_place(q=128, k=0, v=384)])
+def test_a_fused_projection_is_turned_in_place(lib, good):
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where nothing can be launched")
+    assert append(lib, **good) == _lib.FA_ERR_CUDA  # the checks pass; there is no device here
+
+
+def test_rows_too_wide_for_32_bits(lib):
+    wide = 1 << 25
+    assert append(lib, c=cache(heads=wide, num_pages=4), ldk=wide * 64, ldv=wide * 64) == UNSUPPORTED
+    assert fwd(lib, T=2, Hq=wide, ldq=wide * 64) == UNSUPPORTED
+
+
+def test_max_q_must_fit_32_bits():
+    class Fake:  # the check comes before any tensor is looked at closely
+        shape = (2, 3)
+
+        def dim(self):
+            return 2
+    for bad in (-1, 1 << 31, (1 << 32) + 1):
+        with pytest.raises(ValueError, match="max_q"):
+            api.PagedBatch(Fake(), None, None, bad)
