@@ -38,6 +38,17 @@ struct AppendParams {
   int subs;         // blocks of a page
 };
 
+// Sequence b's new rows: none where their positions cannot be trusted (a length below 0, beyond the block table or
+// below the rows), since live tokens of this sequence, or of one that shares its full pages, lie at any others.
+FA_HD SeqInfo append_seq(const PagedBatch& p, int b) {
+  SeqInfo s = load_seq(p, b);
+  if (s.rows > 0 && (s.cut || s.len < s.rows)) {
+    s.rows = 0;
+    record(p.status, kBadLength);
+  }
+  return s;
+}
+
 // This lane's 8 columns as fp32 pairs.
 struct Eight {
   float2 v[4];
@@ -170,13 +181,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads ? 4 : 1) ap
   rest = q;
   const int h = FP8 ? i1 : i0, blk = FP8 ? i0 : i1;
   const int b = rest / static_cast<unsigned>(prm.max_touched), ordinal = rest - b * prm.max_touched;
-  const SeqInfo s = load_seq(pb, b);
+  const SeqInfo s = append_seq(pb, b);
   const int start = s.len - s.rows;  // position of the first new row
   if (s.rows == 0) return;
-  if (start < 0) {
-    record(pb.status, kBadLength);
-    return;
-  }
   const int block = (start >> pb.page_shift) + ordinal;
   const int base = block << pb.page_shift;  // position of the page's first slot
   if (base >= s.len) return;

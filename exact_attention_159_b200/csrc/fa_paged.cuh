@@ -47,6 +47,7 @@ struct PagedBatch {
 
 struct SeqInfo {
   int row0, rows, len;  // first token row, new rows, tokens in all
+  bool cut;             // the length is not the one given, which was below 0 or beyond the block table
 };
 
 FA_HD void record(int* status, int what) {
@@ -57,8 +58,8 @@ FA_HD void record(int* status, int what) {
 #endif
 }
 
-// Sequence b, reduced to what is safe to follow: no rows where cu_q cannot be trusted, and no more keys
-// than the block table names.
+// Sequence b, reduced to what is safe to read: no rows where cu_q cannot be trusted, and no more keys than the
+// block table names (a length cut to it moves the new rows' positions, so nothing may be written by it).
 FA_HD SeqInfo load_seq(const PagedBatch& p, int b) {
   SeqInfo s;
   const int r0 = p.cu_q[b], r1 = p.cu_q[b + 1];
@@ -70,7 +71,8 @@ FA_HD SeqInfo load_seq(const PagedBatch& p, int b) {
     record(p.status, kBadRows);
   }
   const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
-  if (s.len < 0 || s.len > cap) {
+  s.cut = s.len < 0 || s.len > cap;
+  if (s.cut) {
     s.len = s.len < 0 ? 0 : static_cast<int>(cap);
     record(p.status, kBadLength);
   }

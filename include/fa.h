@@ -233,8 +233,10 @@ int fa_convert_f32_bf16(const float* x, void* y, int64_t n, void* stream);
  *
  * The kernels check what they read there: a cu_q that decreases, leaves [0, T]
  * or exceeds max_q (detail 0xE01: that sequence is left out), a length below
- * zero, beyond the table or, in fa_cache_append, below the new tokens (0xE02),
- * a page number outside [0, num_pages) (0xE03: its tokens are not written; in
+ * zero, beyond the table or, in fa_cache_append, below the new tokens (0xE02:
+ * fa_cache_append leaves that sequence out, keys, values and queries;
+ * fa_fwd_paged counts the length as 0, or as what the table holds), a page
+ * number outside [0, num_pages) (0xE03: its tokens are not written; in
  * fa_fwd_paged that sequence's results are unspecified), a position beyond the
  * rotation's tables (0xE04: the token is left out).  fa_last_device_status
  * reports them as FA_ERR_INDEX; memory outside the given tensors is never

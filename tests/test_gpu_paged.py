@@ -632,3 +632,35 @@ def test_same_call_gives_the_same_bits_and_streams_do_not_meet(q_lens):
     torch.cuda.synchronize()
     for o, l in got:
         assert torch.equal(o, want) and torch.equal(l, wl)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("q_len", [1, 3, 150])
+@pytest.mark.parametrize("length", [161, 170, 10 ** 6, 2 ** 31 - 1, -3, -2 ** 31])
+def test_append_leaves_out_a_sequence_of_a_length_its_table_does_not_hold(e4m3, q_len, length):
+    """Its table is full of valid pages, the last one shared with another sequence (as a full one may be): no byte of
+    them, no scale and no query row of that sequence is written; the other sequences' tokens are."""
+    bt = Batch([3, q_len, 1], [40, 160, 9], 4, 2, 64, 16, e4m3, seed=43, dead=None)
+    bt.table[0, 0] = bt.table[1, 9]
+    g = torch.Generator().manual_seed(q_len)
+    k, v, q = (torch.randn(bt.T, h, 64, generator=g).bfloat16().cuda() * 4 for h in (2, 2, 4))
+    angle = torch.rand(160, 32, generator=g).cuda()
+    mine = torch.zeros(bt.T, dtype=torch.bool, device="cuda")
+    mine[3:3 + q_len] = True
+
+    def run(rows, batch, cache):
+        out = torch.full((len(rows), 4, 64), 5.0, device="cuda").bfloat16()
+        api.fa_cache_append(k[rows], v[rows], cache, batch, cos=angle.cos(), sin=angle.sin(), q=q[rows], q_out=out)
+        return _status(), out, [x.view(torch.uint8).clone() for x in (bt.dk, bt.dv, bt.dks, bt.dvs) if x is not None]
+
+    cache, batch, _ = bt.dev()
+    batch.seq_lens[1] = length
+    st, got_q, got = run(torch.arange(bt.T, device="cuda"), batch, cache)
+    assert st == (_lib.FA_ERR_INDEX, 0xE02)
+    assert bool((got_q[mine] == 5).all())
+    cache, batch, _ = bt.dev()  # the same without that sequence's tokens
+    batch.cu_q.copy_(torch.tensor([0, 3, 3, 4], dtype=torch.int32))
+    st, want_q, want = run((~mine).nonzero()[:, 0], batch, cache)
+    assert st == (0, 0) and torch.equal(got_q[~mine], want_q)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)

@@ -172,3 +172,21 @@ def test_max_q_must_fit_32_bits():
     for bad in (-1, 1 << 31, (1 << 32) + 1):
         with pytest.raises(ValueError, match="max_q"):
             api.PagedBatch(Fake(), None, None, bad)
+
+
+# ------------------------------------------------------------------- sequences that an append leaves out
+def run_on_the_host(source, tmp_path, *flags):
+    """Compiles a host program of this folder with the kernels' headers and runs it."""
+    import os
+    import subprocess
+    exe = str(tmp_path / "program")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "-O1", "-I", build.CSRC, "-o", exe, os.path.join(here, source),
+                    *flags], check=True, capture_output=True, text=True)
+    done = subprocess.run([exe], capture_output=True, text=True)
+    assert done.returncode == 0 and "ok" in done.stdout, done.stdout + done.stderr
+
+
+def test_lengths_that_an_append_leaves_out(tmp_path):
+    """Beyond the block table by one token or by far, below zero, below the new tokens: no row is taken."""
+    run_on_the_host("paged_append_host.cu", tmp_path)
