@@ -61,6 +61,16 @@ __device__ __forceinline__ float4 page_scales(float ks, float vs) {
   return make_float4(ks, lv, (tiny ? kUnboost : 1.0f) / vs, tiny ? kBoost : 0.0f);
 }
 
+// 2^d for d <= 0 as two factors, the second 1 down to the smallest normal.  A softmax's sum counts a key by 1 / (its
+// value scale), up to 2^100, in units of a reference that holds the scale's logarithm: when the reference moves from
+// a page of zeros to one of scale 2^60, by 2^-160, what that leaves of the sum still counts, and the one factor would
+// flush to zero.  (O's terms hold no 1 / scale: what flushes there is nothing beside the largest weight's rounding.)
+struct Exp2Pair {
+  float a, b;
+  __device__ __forceinline__ explicit Exp2Pair(float d) : a(exp2_sfu(fmaxf(d, -126.0f))), b(exp2_sfu(fminf(d + 126.0f, 0.0f))) {}
+  __device__ __forceinline__ float times(float x) const { return x * a * b; }
+};
+
 // What the join needs of the cut before share c, left in the workspace by CTA c, whose share begins with tile
 // `tile` of an item of n.
 struct alignas(16) CutPlan {
@@ -311,9 +321,10 @@ __device__ __forceinline__ void meet(DecodeAcc<D, NT>& a, uint8_t* box, int lane
       for (int e = 0; e < 2; ++e) {
         const float mx = fmaxf(a.m[n][e], mb[e]);
         const float ms = mx == -INFINITY ? 0.0f : mx;
-        ca[e] = exp2_sfu(a.m[n][e] - ms);
-        cb[e] = exp2_sfu(mb[e] - ms);
-        a.l[n][e] = a.l[n][e] * ca[e] + lb[e] * cb[e];
+        const Exp2Pair pa(a.m[n][e] - ms), pb(mb[e] - ms);
+        ca[e] = pa.times(1.0f);
+        cb[e] = pb.times(1.0f);
+        a.l[n][e] = pa.times(a.l[n][e]) + pb.times(lb[e]);
         a.m[n][e] = mx;
       }
 #pragma unroll
@@ -630,9 +641,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
               m = fmaxf(m, acc.m[n][e]);
-              al[e] = m == -INFINITY ? 1.0f : exp2_sfu(acc.m[n][e] - m);
+              const Exp2Pair by(m == -INFINITY ? 0.0f : acc.m[n][e] - m);
+              al[e] = by.times(1.0f);
               acc.m[n][e] = m;
-              acc.l[n][e] *= al[e];
+              acc.l[n][e] = by.times(acc.l[n][e]);
             }
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {

@@ -65,8 +65,9 @@ __device__ __forceinline__ void join_row(const JoinItem& it, int lr, int begin, 
   for (int k0 = 0; k0 < n; k0 += 32) {
     const float2 ml = k0 + lane < n ? it.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.0f);
     // l = 0: the row sees no key of the part, whose O may not be written
-    const float w = ml.y == 0.0f ? 0.0f : exp2_sfu(ml.x - (m == -INFINITY ? 0.0f : m));
-    l = fmaf(w, ml.y, l);
+    const Exp2Pair by(ml.x - (m == -INFINITY ? 0.0f : m));
+    const float w = ml.y == 0.0f ? 0.0f : by.times(1.0f);
+    l += by.times(ml.y);
     const int here = min(32, n - k0);
 #pragma unroll 8
     for (int k = begin; k < here; k += stride) {

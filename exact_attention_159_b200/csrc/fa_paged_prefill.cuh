@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(384, 1)
         const bool need = m_new > m_ref + kRescaleTau;
         const float alpha = need ? exp2_sfu(m_ref - m_new) : 1.0f;
         if (need) {
-          l *= alpha;
+          l = FP8 ? Exp2Pair(m_ref - m_new).times(l) : l * alpha;
           m_ref = m_new;
         }
         const float m_sub = m_ref == -INFINITY ? 0.0f : m_ref;
@@ -963,8 +963,9 @@ __global__ void __launch_bounds__(384, 1)
         if (t == 0 && t0 + 1 < end) {
           const float2 other = ml[r];
           const float m = fmaxf(m_ref, other.x), ms = m == -INFINITY ? 0.0f : m;
-          const float ca = exp2_sfu(m_ref - ms), cb = exp2_sfu(other.x - ms);
-          l = l * ca + other.y * cb;
+          const Exp2Pair pa(m_ref - ms), pb(other.x - ms);
+          const float ca = pa.times(1.0f), cb = pb.times(1.0f);
+          l = pa.times(l) + pb.times(other.y);
           m_ref = m;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {

@@ -664,3 +664,25 @@ def test_append_leaves_out_a_sequence_of_a_length_its_table_does_not_hold(e4m3, 
     assert st == (0, 0) and torch.equal(got_q[~mine], want_q)
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("big", [20, 27, 40, 60])
+@pytest.mark.parametrize("order", ["zeros first", "zeros last", "alternating"])
+@pytest.mark.parametrize("q_lens,lens,page", [([1, 1], [300, 257], 128), ([1, 3], [130, 250], 32), ([1, 2], [20000, 90], 64),
+                                              ([70, 300], [500, 777], 32), ([20], [9000], 128), ([70], [6000], 16)])
+def test_pages_of_zeros_beside_large_scales(big, order, q_lens, lens, page):
+    """A page of zeros has no weight in O but all of its weight in the softmax's sum, whatever the other pages' value
+    scales: over one key tile (by different warps), several, and several shares joined, in any order."""
+    def vscale(bt, g):
+        s = torch.full((bt.n_pages, bt.Hkv), 2.0 ** big)
+        for b, n in enumerate(bt.lens):
+            used = -(-n // bt.page)
+            for i in range(used):
+                zero = {"zeros first": i < used // 2, "zeros last": i >= (used + 1) // 2, "alternating": i % 2 == 0}[order]
+                if zero:
+                    s[int(bt.table[b, i])] = 0.0
+        return s
+
+    bt = Batch(q_lens, lens, 8, 2, 128, page, True, seed=25, vscale=vscale, dead=None)
+    out, lse, scale = attend(bt)
+    check(bt, out, lse, scale, True, f"zeros beside 2^{big}, {order}, {q_lens} {lens}")
