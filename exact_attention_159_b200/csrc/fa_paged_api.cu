@@ -68,13 +68,27 @@ int check_paged(const fa_paged_cache* c, const fa_paged_batch* b, int T, int Hq,
   return FA_OK;
 }
 
+bool meets_batch(const void* p, size_t n, const fa_paged_batch* b, const Sizes& z) {
+  return overlaps(p, n, b->block_table, z.table) || overlaps(p, n, b->cu_q, (static_cast<size_t>(b->B) + 1) * 4) ||
+         overlaps(p, n, b->seq_lens, static_cast<size_t>(b->B) * 4);
+}
+
 // A written range against everything of the cache and the batch.
 bool meets(const void* p, size_t n, const fa_paged_cache* c, const fa_paged_batch* b, const Sizes& z) {
   if (overlaps(p, n, c->K, z.cache) || overlaps(p, n, c->V, z.cache)) return true;
   if (c->type == FA_CACHE_E4M3 && (overlaps(p, n, c->K_scale, z.scales) || overlaps(p, n, c->V_scale, z.scales)))
     return true;
-  return overlaps(p, n, b->block_table, z.table) || overlaps(p, n, b->cu_q, (static_cast<size_t>(b->B) + 1) * 4) ||
-         overlaps(p, n, b->seq_lens, static_cast<size_t>(b->B) * 4);
+  return meets_batch(p, n, b, z);
+}
+
+// The ranges that an append writes against one another and the batch's arrays (check_paged has K against V).
+bool written_meet(const fa_paged_cache* c, const fa_paged_batch* b, const Sizes& z) {
+  if (meets_batch(c->K, z.cache, b, z) || meets_batch(c->V, z.cache, b, z)) return true;
+  if (c->type != FA_CACHE_E4M3) return false;
+  for (const float* p : {c->K_scale, c->V_scale})
+    if (overlaps(p, z.scales, c->K, z.cache) || overlaps(p, z.scales, c->V, z.cache) || meets_batch(p, z.scales, b, z))
+      return true;
+  return overlaps(c->K_scale, z.scales, c->V_scale, z.scales);
 }
 
 size_t rows_bytes(int T, int64_t ld, int heads, int d) {
@@ -280,7 +294,8 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
     if (ld > (1LL << 40) / T) return FA_ERR_UNSUPPORTED;
   const size_t kb = rows_bytes(T, ldk, Hkv, d), vb = rows_bytes(T, ldv, Hkv, d);
   const size_t tb = static_cast<size_t>(n_pos) * (rot_dim / 2) * 4;
-  if (meets(K, kb, cache, batch, z) || meets(V, vb, cache, batch, z)) return FA_ERR_INVALID_ARG;
+  if (written_meet(cache, batch, z) || meets(K, kb, cache, batch, z) || meets(V, vb, cache, batch, z))
+    return FA_ERR_INVALID_ARG;
   if (Q) {
     const size_t qb = rows_bytes(T, ldq, Hq, d), ob = rows_bytes(T, ldqo, Hq, d);
     if (meets(Q, qb, cache, batch, z) || meets(Q_out, ob, cache, batch, z)) return FA_ERR_INVALID_ARG;

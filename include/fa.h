@@ -295,7 +295,9 @@ typedef struct {
  * two sequences that share pages may share full ones only.  Q_out may not
  * overlap the cache or, unless in place, Q, K or V; in place, Q's rows may lie
  * side by side with K's and V's at one stride, but share no element with them.
- * The cache may not overlap any input.  One launch.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
+ * The cache may not overlap any input, and its own arrays not one another:
+ * K_scale and V_scale are two (one for both serves fa_fwd_paged only).  One
+ * launch.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
  */
 int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, const void* K, int64_t ldk,
                     const void* V, int64_t ldv, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo, int Hq,

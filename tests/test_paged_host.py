@@ -190,3 +190,37 @@ def run_on_the_host(source, tmp_path, *flags):
 def test_lengths_that_an_append_leaves_out(tmp_path):
     """Beyond the block table by one token or by far, below zero, below the new tokens: no row is taken."""
     run_on_the_host("paged_append_host.cu", tmp_path)
+
+
+# ------------------------------------------------------------- what an append writes overlaps nothing else
+passes = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where nothing can be launched")
+SCALES, PAGES = 10 * 2 * 4, 10 * 2 * 16 * 64  # bytes of the cache() above: a scale tensor, e4m3 pages
+
+
+@pytest.mark.parametrize("bad", [
+    dict(c=cache(V_scale=A[2])), dict(c=cache(V_scale=A[2] + SCALES - 4)), dict(c=cache(K_scale=A[3] + 4)),
+    dict(c=cache(K_scale=A[0])), dict(c=cache(K_scale=A[0] + PAGES - 4)), dict(c=cache(K_scale=A[1] + 64)),
+    dict(c=cache(V_scale=A[0] + 64)), dict(c=cache(V_scale=A[1] - SCALES + 4)),
+    dict(b=batch(block_table=A[0])), dict(b=batch(block_table=A[1] + PAGES - 4)), dict(b=batch(block_table=A[2])),
+    dict(b=batch(cu_q=A[0] + 16)), dict(b=batch(cu_q=A[3])), dict(b=batch(seq_lens=A[1])), dict(b=batch(seq_lens=A[2] - 8)),
+    dict(c=cache(e4m3=False), b=batch(seq_lens=A[0] + PAGES)),  # bf16 pages are twice as large
+])
+def test_appends_whose_written_ranges_overlap_are_refused(lib, bad):
+    """One scale tensor for keys and values (each would be stored over the other), scales among pages, pages or scales
+    among the index arrays."""
+    assert append(lib, **bad) == INVALID
+    assert append(lib, **dict(Q_ARGS, **bad)) == INVALID
+
+
+@passes
+@pytest.mark.parametrize("good", [
+    dict(c=cache(V_scale=A[2] + SCALES)), dict(c=cache(K_scale=A[0] + PAGES)), dict(b=batch(block_table=A[0] + PAGES)),
+    dict(c=cache(e4m3=False, K_scale=A[2], V_scale=A[2])), dict(c=cache(e4m3=False, K_scale=A[0], V_scale=A[1])),
+])
+def test_appends_whose_ranges_meet_or_are_not_used_pass_the_checks(lib, good):
+    assert append(lib, **good) == _lib.FA_ERR_CUDA
+
+
+@passes
+def test_attention_reads_one_scale_tensor_for_both(lib):
+    assert fwd(lib, c=cache(V_scale=A[2])) == _lib.FA_ERR_CUDA
