@@ -276,12 +276,13 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
                     const float* cosine, const float* sine, int rot_dim, int interleaved, int n_pos, void* stream) {
   bool empty = false;
   Sizes z;
-  int rc = check_paged(cache, batch, T, Hq, Q != nullptr, &empty, &z);
+  int rc = check_paged(cache, batch, T, Hq, Q != nullptr && Hq > 0, &empty, &z);
   if (rc != FA_OK) return rc;
   if (rot_dim < 0 || n_pos < 0 || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
   if (rot_dim > cache->d || rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
   if ((Q == nullptr) != (Q_out == nullptr) || (Q ? rot_dim == 0 : Hq != 0)) return FA_ERR_INVALID_ARG;
   if (empty) return FA_OK;
+  if (Hq == 0) Q = Q_out = nullptr;  // no head to turn, but keys and values to append
   if (!K || !V || (rot_dim > 0 && (!cosine || !sine))) return FA_ERR_INVALID_ARG;
   const int Hkv = cache->heads, d = cache->d;
   const int64_t kv_row = static_cast<int64_t>(Hkv) * d, q_row = static_cast<int64_t>(Hq) * d;

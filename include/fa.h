@@ -276,7 +276,7 @@ typedef struct {
  * d, multiples of 8), so slices of a fused projection serve as they are.  Q:
  * bf16 [T, Hq, d], rows ldq apart, or NULL; Q_out: bf16 [T, Hq, d], rows ldqo
  * apart (Q_out == Q with ldqo == ldq rotates in place).  Hq a multiple of
- * heads (0 without Q).
+ * heads (0 without Q; with 0 Q is not read).
  * cosine, sine: fp32 [n_pos, rot_dim / 2], 16-byte aligned, the angles' cosines and sines
  * of each position; rot_dim <= d, a multiple of 16 (0: no rotation, and no Q).
  * The first rot_dim columns turn in pairs, x_i' = x_i cos - x_j sin, x_j' =

@@ -686,3 +686,25 @@ def test_pages_of_zeros_beside_large_scales(big, order, q_lens, lens, page):
     bt = Batch(q_lens, lens, 8, 2, 128, page, True, seed=25, vscale=vscale, dead=None)
     out, lse, scale = attend(bt)
     check(bt, out, lse, scale, True, f"zeros beside 2^{big}, {order}, {q_lens} {lens}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_with_no_query_heads_appends_the_keys_and_values(e4m3):
+    """Q with zero heads (given to the library by pointer) has nothing to turn; the keys and values are appended."""
+    import ctypes
+    bt = Batch([3, 1], [40, 17], 4, 2, 64, 16, e4m3, seed=44, dead=None)
+    k, v, q = (torch.randn(4, 2, 64, device="cuda").bfloat16() for _ in range(3))
+    cos, sin = torch.ones(48, 32, device="cuda"), torch.zeros(48, 32, device="cuda")
+    cache, batch, _ = bt.dev()
+    assert api.fa_cache_append(k, v, cache, batch, cos=cos, sin=sin) is None
+    want = [bt.dk.view(torch.uint8), bt.dv.view(torch.uint8)]
+    assert _status() == (0, 0)
+    assert not torch.equal(want[0].cpu(), bt.k.view(torch.uint8)) and not torch.equal(want[1].cpu(), bt.v.view(torch.uint8))
+    cache, batch, _ = bt.dev()
+    q_out = torch.full_like(q, 5.0)
+    rc = _lib.lib().fa_cache_append(cache._ref, batch._ref, 4, k.data_ptr(), 128, v.data_ptr(), 128, q.data_ptr(), 128,
+                                    q_out.data_ptr(), 128, 0, cos.data_ptr(), sin.data_ptr(), 64, 0, 48,
+                                    ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == _lib.FA_OK and _status() == (0, 0)
+    assert torch.equal(bt.dk.view(torch.uint8), want[0]) and torch.equal(bt.dv.view(torch.uint8), want[1])
+    assert bool((q_out == 5).all())

@@ -224,3 +224,17 @@ def test_appends_whose_ranges_meet_or_are_not_used_pass_the_checks(lib, good):
 @passes
 def test_attention_reads_one_scale_tensor_for_both(lib):
     assert fwd(lib, c=cache(V_scale=A[2])) == _lib.FA_ERR_CUDA
+
+
+@passes
+def test_an_append_with_queries_of_no_heads_is_not_empty(lib):
+    """Q with zero heads has nothing to turn, but there are keys and values to append."""
+    assert append(lib, **dict(Q_ARGS, Hq=0)) == _lib.FA_ERR_CUDA  # the checks pass; there is no device here
+    assert append(lib, **dict(Q_ARGS, Hq=0, ldq=0, ldqo=0)) == _lib.FA_ERR_CUDA
+
+
+def test_queries_of_no_heads_are_checked_like_others(lib):
+    assert append(lib, **dict(Q_ARGS, Hq=0, Qo=None)) == INVALID
+    assert append(lib, **dict(Q_ARGS, Hq=0, K=A[0])) == INVALID
+    assert append(lib, **dict(Q_ARGS, Hq=0), T=0) == OK
+    assert fwd(lib, Hq=0) == OK
