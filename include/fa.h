@@ -324,7 +324,9 @@ int fa_cache_append(const fa_paged_cache* cache, const fa_paged_batch* batch, in
  * workspace: device memory of at least fa_fwd_paged_workspace_size() bytes,
  * 16-byte aligned; contents on entry do not matter, and calls that may overlap
  * in time must not share one (two captured graphs included).  The size depends
- * on (heads, d, page_size, Hq, T, B, max_pages, max_q) only.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
+ * on the cache's (type, heads, d, page_size) and (Hq, T, B, max_pages, max_q)
+ * only: a bf16 cache needs the parts of many rows from fewer rows on than an
+ * e4m3 one.  T, B or heads equal to 0, or max_q = 0: nothing is launched.
  */
 size_t fa_fwd_paged_workspace_size(const fa_paged_cache* cache, const fa_paged_batch* batch, int T, int Hq);
 int fa_fwd_paged(const void* Q, int64_t ldq, const fa_paged_cache* cache, const fa_paged_batch* batch, int T, void* O,

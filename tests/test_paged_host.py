@@ -238,3 +238,28 @@ def test_queries_of_no_heads_are_checked_like_others(lib):
     assert append(lib, **dict(Q_ARGS, Hq=0, K=A[0])) == INVALID
     assert append(lib, **dict(Q_ARGS, Hq=0), T=0) == OK
     assert fwd(lib, Hq=0) == OK
+
+
+# ------------------------------------------------------------------------------------- the workspace
+def test_workspace_sizes_follow_the_cache_type(lib):
+    """The kernel of many rows takes more than 16 rows of a bf16 cache and more than 32 of an e4m3 one, and only a call
+    that may have as many needs its parts; fa.h names what the size depends on, the type among it."""
+    def size(e4m3, rows, **kw):  # rows: new tokens x query heads of a key/value head
+        c, b = cache(e4m3, d=128, **kw), batch(max_q=rows)
+        return lib.fa_fwd_paged_workspace_size(ctypes.byref(c), ctypes.byref(b), 40, 2)
+
+    few, parts = size(False, 16), 2 * 148 * 256 * (128 * 4 + 8)
+    for e4m3, last_few in ((False, 16), (True, 32)):
+        for rows in (1, 16, 17, 32, 33, 40):
+            assert size(e4m3, rows) == few + (parts if rows > last_few else 0), (e4m3, rows)
+            assert size(e4m3, rows, num_pages=77) == size(e4m3, rows)
+            need = size(e4m3, rows)
+            args = dict(c=cache(e4m3, d=128), b=batch(max_q=rows), T=40, Hq=2, W=A[15])
+            assert fwd(lib, wsb=need - 1, **args) == INVALID
+            if not torch.cuda.is_available():
+                assert fwd(lib, wsb=need, **args) == _lib.FA_ERR_CUDA  # the checks pass; there is no device here
+    import os
+    with open(os.path.join(build.ROOT, "include", "fa.h")) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    says = text[text.index("The size depends on"):]
+    assert "type" in says[:says.index(" only")]
