@@ -232,7 +232,27 @@ def fa_bwd_finish(workspace, B: int, Hq: int, Nq: int, d: int, scale: float | No
     return out
 
 
-class PagedCache:
+class _Handle:
+    """Tensors as the library is told of them, once: the attributes are not assigned again and the tensors stay in
+    their memory (what they hold is read by every call)."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{name} of a {type(self).__name__} is fixed: make another one")
+        super().__setattr__(name, value)
+
+    def _describe(self, struct, tensors):
+        self._c, self._ref = struct, ctypes.byref(struct)
+        self._places = tuple((t.data_ptr, t.data_ptr()) for t in tensors if t is not None)
+
+    def _check_places(self):
+        for at, was in self._places:
+            if at() != was:
+                raise ValueError(f"a tensor of this {type(self).__name__} has left its memory (resized or given other "
+                                 "storage): make another one")
+
+
+class PagedCache(_Handle):
     """A paged key/value cache: k_pages, v_pages [num_pages, Hkv, page_size, d], bf16, or float8_e4m3fn
     with k_scale, v_scale fp32 [num_pages, Hkv] (a held value stands for code * scale; two tensors where
     tokens are appended, one for both is enough to attend).  page_size 16, 32, 64 or 128; d 64 or 128.  Holds the tensors and describes them to the library; the caller hands
@@ -258,16 +278,16 @@ class PagedCache:
         self.num_pages, self.heads, self.page_size, self.d = pages, heads, size, d
         self.device = k_pages.device
         self._index = k_pages.get_device()
-        self._c = _lib.CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr() if fp8 else None,
-                                   v_scale.data_ptr() if fp8 else None,
-                                   _lib.FA_CACHE_E4M3 if fp8 else _lib.FA_CACHE_BF16, pages, heads, size, d)
-        self._ref = ctypes.byref(self._c)
+        self._describe(_lib.CacheStruct(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                        _lib.FA_CACHE_E4M3 if fp8 else _lib.FA_CACHE_BF16, pages, heads, size, d),
+                       (k_pages, v_pages, k_scale, v_scale))
 
 
-class PagedBatch:
+class PagedBatch(_Handle):
     """B sequences of a paged cache: block_table int32 [B, max_pages], cu_q int32 [B + 1] (the token rows
     of each), seq_lens int32 [B] (tokens in all, the new ones last), max_q (no sequence has more new
-    tokens).  The tensors are read when the kernels run: refill them in place from step to step."""
+    tokens).  The tensors are read when the kernels run: refill them in place from step to step (max_q and the
+    tensors themselves are fixed; a batch of another size is another PagedBatch)."""
 
     def __init__(self, block_table, cu_q, seq_lens, max_q: int):
         if block_table.dim() != 2:
@@ -282,9 +302,8 @@ class PagedBatch:
         self.B, self.max_pages, self.max_q = B, max_pages, int(max_q)
         self.device = block_table.device
         self._index = block_table.get_device()
-        self._c = _lib.BatchStruct(block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), B, max_pages,
-                                   self.max_q)
-        self._ref = ctypes.byref(self._c)
+        self._describe(_lib.BatchStruct(block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), B, max_pages,
+                                        self.max_q), (block_table, cu_q, seq_lens))
 
 
 def _need_rows(t: torch.Tensor, name: str, heads: int, d: int, rows: int, device: int) -> int:
@@ -320,10 +339,12 @@ def _empty(like, shape, dtype, stream):
 
 
 def _same_device(cache: PagedCache, batch: PagedBatch) -> int:
-    """The current device, which the cache and the batch have to be on."""
+    """The current device, which the cache and the batch have to be on, in the memory that they were made with."""
     cur = torch._C._cuda_getDevice()
     if cache._index != cur or batch._index != cur:
         raise ValueError(f"cache on {cache.device}, batch on {batch.device}, but the current device is cuda:{cur}")
+    cache._check_places()
+    batch._check_places()
     return cur
 
 

@@ -263,3 +263,37 @@ def test_workspace_sizes_follow_the_cache_type(lib):
         text = " ".join(f.read().replace("*", " ").split())
     says = text[text.index("The size depends on"):]
     assert "type" in says[:says.index(" only")]
+
+
+# ---------------------------------------------------------------------------------- what a handle stands for
+@pytest.fixture
+def handles(monkeypatch):
+    """A cache and a batch of host tensors, for the binding's own checks: no call gets as far as a device."""
+    monkeypatch.setattr(api, "_need", lambda *a: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    pages = [torch.zeros((4, 2, 16, 64), dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2)]
+    return api.PagedCache(*pages, torch.ones(4, 2), torch.ones(4, 2)), api.PagedBatch(i(2, 3), i(3), i(2), 1)
+
+
+def test_handles_are_not_changed_without_effect(handles):
+    """The library is told what the handle was made of: assigning to it would change nothing of the next call."""
+    for handle, names in zip(handles, (("k_pages", "v_pages", "k_scale", "v_scale", "num_pages", "page_size"),
+                                       ("block_table", "cu_q", "seq_lens", "max_q", "B", "max_pages"))):
+        for name in names:
+            was = getattr(handle, name)
+            with pytest.raises(AttributeError, match=name):
+                setattr(handle, name, was)
+            assert getattr(handle, name) is was
+
+
+@pytest.mark.parametrize("which,name", [(0, "k_pages"), (0, "v_pages"), (0, "k_scale"), (0, "v_scale"), (1, "block_table"),
+                                        (1, "cu_q"), (1, "seq_lens")])
+def test_tensors_that_have_left_their_memory_are_refused(handles, which, name):
+    t = getattr(handles[which], name)
+    x = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    t.data = torch.zeros_like(t)  # as a tensor resized in place: the memory that was described may be another's by now
+    with pytest.raises(ValueError, match="memory"):
+        api.fa_cache_append(x, x, *handles)
+    with pytest.raises(ValueError, match="memory"):
+        api.fa_fwd_paged(x, *handles)
