@@ -101,23 +101,28 @@ struct MapCache {
   CUtensorMap map[kSlots];
   int used = 0, next = 0;
 };
-static MapCache g_maps;
+// Pages' maps are kept apart: a model has a cache for each layer, and their maps would put out those of the
+// contiguous operands, which a step uses again.
+static MapCache g_maps[2];
+static MapCache& maps_of(const MapKey& k) { return g_maps[k.kind >= kMapPages ? 1 : 0]; }
 
 bool map_lookup(const MapKey& k, CUtensorMap* out) {
-  std::lock_guard<std::mutex> lock(g_maps.mu);
-  for (int i = 0; i < g_maps.used; ++i)
-    if (g_maps.key[i] == k) {
-      *out = g_maps.map[i];
+  MapCache& c = maps_of(k);
+  std::lock_guard<std::mutex> lock(c.mu);
+  for (int i = 0; i < c.used; ++i)
+    if (c.key[i] == k) {
+      *out = c.map[i];
       return true;
     }
   return false;
 }
 void map_store(const MapKey& k, const CUtensorMap& m) {
-  std::lock_guard<std::mutex> lock(g_maps.mu);
-  const int i = g_maps.used < MapCache::kSlots ? g_maps.used++ : g_maps.next;
-  if (i == g_maps.next) g_maps.next = (g_maps.next + 1) % MapCache::kSlots;
-  g_maps.key[i] = k;
-  g_maps.map[i] = m;
+  MapCache& c = maps_of(k);
+  std::lock_guard<std::mutex> lock(c.mu);
+  const int i = c.used < MapCache::kSlots ? c.used++ : c.next;
+  if (i == c.next) c.next = (c.next + 1) % MapCache::kSlots;
+  c.key[i] = k;
+  c.map[i] = m;
 }
 
 // The dynamic shared memory limit of a kernel is a per-device attribute: set it once per (kernel,

@@ -26,7 +26,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 // Encoded tensor maps of recent calls, keyed by (address, extents, box, element kind): callers that
 // reuse their buffers (training loops, graph replays, the ring steps, a cache) skip cuTensorMapEncodeTiled.
 // A map holds only the address and geometry it was encoded from, so a hit is exactly the map a
-// fresh encode would produce.  Small, round-robin replacement, one lock.
+// fresh encode would produce.  Small, round-robin replacement, one lock for the operands' maps and one for the pages'.
+constexpr int kMapPages = 2;  // kinds from here on are cache pages
 struct MapKey {
   const void* base;
   // kind 0: bf16 operand, 1: fp32 dQ accumulator, 2 / 3: bf16 / e4m3 cache pages (BH pages * heads, N = page size)

@@ -129,7 +129,7 @@ fa::PagedBatch device_batch(const fa_paged_cache* c, const fa_paged_batch* b, in
 // is 64 bytes) x `rows` slots, swizzled by the box's width.
 bool make_page_map(CUtensorMap* map, const void* base, const fa_paged_cache* c, int rows) {
   const bool fp8 = c->type == FA_CACHE_E4M3;
-  const MapKey key{base, c->num_pages * c->heads, c->page_size, c->d, rows, fp8 ? 3 : 2};
+  const MapKey key{base, c->num_pages * c->heads, c->page_size, c->d, rows, kMapPages + (fp8 ? 1 : 0)};
   if (map_lookup(key, map)) return true;
   auto fn = encode_fn();
   if (!fn) return false;

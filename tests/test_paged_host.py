@@ -297,3 +297,39 @@ def test_tensors_that_have_left_their_memory_are_refused(handles, which, name):
         api.fa_cache_append(x, x, *handles)
     with pytest.raises(ValueError, match="memory"):
         api.fa_fwd_paged(x, *handles)
+
+
+# ------------------------------------------------------------------------------- tensor maps kept by the host
+def test_many_caches_do_not_put_out_the_other_calls_tensor_maps(lib):
+    """A model has a cache for each layer and every cache its maps: the maps that the contiguous forward and backward
+    reuse from call to call stay beside any number of them."""
+    class Key(ctypes.Structure):  # fa_host::MapKey
+        _fields_ = [("base", ctypes.c_void_p)] + [(n, ctypes.c_int) for n in ("BH", "N", "d", "rows", "kind")]
+
+    store = getattr(lib, "_ZN7fa_host9map_storeERKNS_6MapKeyERK14CUtensorMap_st")
+    lookup = getattr(lib, "_ZN7fa_host10map_lookupERKNS_6MapKeyEP14CUtensorMap_st")
+    store.argtypes = lookup.argtypes = [ctypes.POINTER(Key), ctypes.c_void_p]
+    store.restype, lookup.restype = None, ctypes.c_bool
+    room = (ctypes.c_uint8 * 512)()
+    at = -(-ctypes.addressof(room) // 64) * 64  # a tensor map is 128 bytes, aligned to 64
+    base = 0x7000_0000_0000
+    operand = lambda i: Key(base + i, 16, 1024, 128, 128, i % 2)  # noqa: E731  kinds 0 and 1: q, k, v, dO; dQ's sums
+    pages = lambda i: Key(base + (1 << 20) + i, 80, 64, 128, 64, 2 + i % 2)  # noqa: E731  kinds 2 and 3
+
+    def put(key, byte):
+        ctypes.memset(at, byte, 128)
+        store(key, at)
+
+    def has(key, byte):
+        ctypes.memset(at + 128, 0, 128)
+        return lookup(key, at + 128) and ctypes.string_at(at + 128, 128) == bytes([byte]) * 128
+
+    for i in range(20):
+        put(operand(i), i + 1)
+    for i in range(160):  # 80 caches, K and V
+        put(pages(i), 200 - i)
+    assert all(has(operand(i), i + 1) for i in range(20))
+    assert has(pages(159), 200 - 159) and not has(pages(0), 200)
+    for i in range(20, 200):
+        put(operand(i), i + 1)
+    assert has(pages(159), 200 - 159)
