@@ -22,9 +22,13 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+def _stream_on(device: int, stream):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 def _stream(stream):
     if stream is None:  # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _stream_on(torch._C._cuda_getDevice(), None)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -237,19 +241,13 @@ class _Handle:
     their memory (what they hold is read by every call)."""
 
     def __setattr__(self, name, value):
-        if name in self.__dict__:
+        if self.__dict__.get(name, value) is not value:  # (`batch.seq_lens += 1` assigns the same tensor again)
             raise AttributeError(f"{name} of a {type(self).__name__} is fixed: make another one")
         super().__setattr__(name, value)
 
     def _describe(self, struct, tensors):
         self._c, self._ref = struct, ctypes.byref(struct)
         self._places = tuple((t.data_ptr, t.data_ptr()) for t in tensors if t is not None)
-
-    def _check_places(self):
-        for at, was in self._places:
-            if at() != was:
-                raise ValueError(f"a tensor of this {type(self).__name__} has left its memory (resized or given other "
-                                 "storage): make another one")
 
 
 class PagedCache(_Handle):
@@ -343,8 +341,11 @@ def _same_device(cache: PagedCache, batch: PagedBatch) -> int:
     cur = torch._C._cuda_getDevice()
     if cache._index != cur or batch._index != cur:
         raise ValueError(f"cache on {cache.device}, batch on {batch.device}, but the current device is cuda:{cur}")
-    cache._check_places()
-    batch._check_places()
+    for handle in (cache, batch):
+        for at, was in handle._places:
+            if at() != was:
+                raise ValueError(f"a tensor of the {type(handle).__name__} has left its memory (resized, or given other "
+                                 "storage): make another one")
     return cur
 
 
@@ -387,7 +388,7 @@ def fa_cache_append(k, v, cache: PagedCache, batch: PagedBatch, cos=None, sin=No
         raise ValueError("q_out is given without q")
     check(_lib.lib().fa_cache_append(cache._ref, batch._ref, T, k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(q), ldq,
                                      _ptr(q_out), ldqo, Hq, _ptr(cos), _ptr(sin), rot, 1 if interleaved else 0,
-                                     n_pos, _stream(stream)), "fa_cache_append")
+                                     n_pos, _stream_on(cur, stream)), "fa_cache_append")
     return q_out
 
 
@@ -424,8 +425,8 @@ def fa_fwd_paged(q, cache: PagedCache, batch: PagedBatch, scale: float | None = 
     else:
         _need(lse, "lse", torch.float32, (T, Hq))
     check(lib.fa_fwd_paged(q.data_ptr(), ldq, cache._ref, batch._ref, T, out.data_ptr(), lse.data_ptr(),
-                           workspace.data_ptr(), ws_bytes, Hq, scale, 1 if causal else 0, _stream(stream)),
-          "fa_fwd_paged")
+                           workspace.data_ptr(), ws_bytes, Hq, scale, 1 if causal else 0,
+                           _stream_on(cur, stream)), "fa_fwd_paged")
     return out, lse
 
 

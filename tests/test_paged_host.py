@@ -283,8 +283,12 @@ def test_handles_are_not_changed_without_effect(handles):
         for name in names:
             was = getattr(handle, name)
             with pytest.raises(AttributeError, match=name):
-                setattr(handle, name, was)
+                setattr(handle, name, was + 1 if isinstance(was, int) else was.clone())
             assert getattr(handle, name) is was
+    batch = handles[1]
+    batch.seq_lens += 1  # in place, and the same tensor assigned again
+    batch.max_q = batch.max_q
+    assert batch.seq_lens.tolist() == [1, 1]
 
 
 @pytest.mark.parametrize("which,name", [(0, "k_pages"), (0, "v_pages"), (0, "k_scale"), (0, "v_scale"), (1, "block_table"),
