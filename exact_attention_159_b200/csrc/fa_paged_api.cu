@@ -171,13 +171,15 @@ int launch_append(const fa::AppendParams& prm, long long units, int most, cudaSt
   const int rows = most < (1 << prm.b.page_shift) ? most : 1 << prm.b.page_shift;  // new tokens that a page can get
   if (rows <= 32 / VPR) return launch_append_blocks<D, FP8, 32, 1>(prm, units, 1, st);
   const int subs = (rows + N / VPR - 1) / (N / VPR);
-  if (!FP8 || subs == 1) return launch_append_blocks<D, FP8, N, 1>(prm, units, subs, st);
-  if constexpr (FP8) {
+  if constexpr (!FP8) {
+    return launch_append_blocks<D, FP8, N, 1>(prm, units, subs, st);
+  } else {
+    constexpr int kMost = 128 / (N / VPR);  // blocks of the longest page: 8, or 4 at D = 64
+    if (subs == 1) return launch_append_blocks<D, FP8, N, 1>(prm, units, 1, st);
     if (subs == 2) return launch_append_blocks<D, FP8, N, 2>(prm, units, 2, st);
     if (subs <= 4) return launch_append_blocks<D, FP8, N, 4>(prm, units, 4, st);
-    return launch_append_blocks<D, FP8, N, 8>(prm, units, 8, st);
+    return launch_append_blocks<D, FP8, N, kMost>(prm, units, kMost, st);
   }
-  return FA_ERR_CUDA;  // not reached
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
