@@ -708,3 +708,60 @@ def test_append_with_no_query_heads_appends_the_keys_and_values(e4m3):
     assert rc == _lib.FA_OK and _status() == (0, 0)
     assert torch.equal(bt.dk.view(torch.uint8), want[0]) and torch.equal(bt.dv.view(torch.uint8), want[1])
     assert bool((q_out == 5).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("q_lens,lens,Hkv,G", [([16], [70001], 1, 8), ([64, 1], [16400, 300], 2, 4)])
+def test_short_chunk_over_a_long_cache_is_joined_from_many_parts(e4m3, q_lens, lens, Hkv, G):
+    """Items of the kernel of many rows cut into more parts than a warp has lanes."""
+    bt = Batch(q_lens, lens, Hkv * G, Hkv, 128, 64, e4m3, seed=26, dead=None)
+    out, lse, scale = attend(bt)
+    check(bt, out, lse, scale, True, f"many parts {q_lens} over {lens} e4m3={e4m3}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_single_tokens_beside_a_long_chunk(e4m3):
+    """Both kernels of one call with work for every SM."""
+    rng = np.random.default_rng(6)
+    lens = rng.integers(100, 3000, 40).tolist()
+    bt = Batch([1] * 20 + [700] + [1] * 19, lens[:20] + [2500] + lens[21:], 8, 2, 128, 32, e4m3, seed=27, dead=None)
+    out, lse, scale = attend(bt)
+    check(bt, out, lse, scale, True, f"tokens beside a chunk e4m3={e4m3}")
+
+
+def test_many_caches_and_two_host_threads():
+    """A cache for each of 40 layers (more tensor maps than the host keeps), in turn and from two threads on two
+    streams: every call's bits are those of the call alone."""
+    import threading
+    bts = [Batch([1, 40, 1], [500, 700 + i, 33], 8, 2, 128, 32, bool(i % 2), seed=100 + i, dead=None) for i in range(40)]
+    handles = [bt.dev() for bt in bts]
+    want = [tuple(x.clone() for x in api.fa_fwd_paged(q, c, b, 0.1)) for c, b, q in handles]
+    assert _status() == (0, 0)
+    for i in (0, 1, 39):
+        check(bts[i], *want[i], 0.1, True, f"cache {i}")
+    same = [False, False]
+
+    def calls(k):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [api.fa_fwd_paged(q, c, b, 0.1) for c, b, q in handles[k::2] * 3]
+            stream.synchronize()
+            same[k] = all(torch.equal(x, y) for o, w in zip(got, want[k::2] * 3) for x, y in zip(o, w))
+
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(same) and _status() == (0, 0)
+
+
+def test_handles_whose_tensors_were_resized_are_refused():
+    bt = Batch([1], [40], 4, 2, 64, 16, True, seed=45)
+    for which, name in ((0, "k_pages"), (0, "v_scale"), (1, "cu_q"), (1, "block_table")):
+        cache, batch, q = bt.dev()
+        getattr((cache, batch)[which], name).resize_(1 << 22)
+        with pytest.raises(ValueError, match="memory"):
+            api.fa_fwd_paged(q, cache, batch)
+        with pytest.raises(ValueError, match="memory"):
+            api.fa_cache_append(q[:, :2], q[:, 2:], cache, batch)
