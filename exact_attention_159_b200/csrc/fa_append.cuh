@@ -14,10 +14,13 @@
 // same warp (a row is D / 8 consecutive lanes) and comes by shuffle, so every input is read once and Q may be
 // rotated in place.  What a block waits for is two dependent loads, the batch's indices and then everything
 // else at once (keys, values, angles, four query heads and the page number); 64 registers keep four blocks on an
-// SM.  One or two new tokens a sequence (a decode batch) take blocks of one warp.  Bound by HBM for prompts
-// (each row is read once and written once) with the instruction rate close behind, by the two loads' latency
-// for single tokens.  22 K tokens of 32 + 2 x 8 heads into pages of 16: bf16 95 us (5.9 of 6.56 TB/s measured
-// copy), e4m3 110 us (4.7 TB/s, 2.5 instructions a cycle); one token 3.2 us.
+// SM, for 16 (bf16) or 36 to 44 bytes (e4m3) of spills a thread.  Batches of no more than two new tokens a sequence
+// (four at D = 64) take blocks of one warp.  Bound by HBM for prompts (each row is read once and written once), in
+// an e4m3 cache by the loads' latency before it (28.7 warps an SM wait for them most of the time; 2.5 of 4
+// instructions a cycle are issued), and by that latency for single tokens.  22 K tokens of 32 + 2 x 8 heads into
+// pages of 16: bf16 95 us (5.9 of 6.56 TB/s measured copy), e4m3 110 to 115 us (4.5 to 4.7 TB/s); one token 3.2 us.
+// The grid has max_q tokens' pages for every sequence: a long prompt among many single tokens launches as many empty
+// blocks.
 #pragma once
 
 #include "fa_paged.cuh"
@@ -112,6 +115,8 @@ __device__ __forceinline__ uint4 pack8_bf16(const Eight& x) {
   return make_uint4(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y),
                     pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y));
 }
+// x times the scale's reciprocal: the quotient itself for a power of two, which every scale is that this kernel wrote;
+// by another (a caller's, kept while it is large enough) a value next to a tie may go to the other neighbour.
 __device__ __forceinline__ uint2 pack8_e4m3(const Eight& x, float inv) {
   const float2 f = make_float2(inv, inv);
   uint32_t h[4];
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kAppendThreads ? 4 : 1) ap
     if (first > 0 && vs > vs_old) rescale_codes(vc, first * D, vs_old / vs, t, THREADS * CL);
     if (live) {
       const size_t at = static_cast<size_t>(slot) * D + vec * 8;
-      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(kx, 1.0f / ks);  // exact for the powers of two written here
+      *reinterpret_cast<uint2*>(kc + at) = pack8_e4m3(kx, 1.0f / ks);
       *reinterpret_cast<uint2*>(vc + at) = pack8_e4m3(unpack8(vraw), 1.0f / vs);
     }
   }

@@ -22,7 +22,7 @@ namespace {
 // Short caches (by the block table's width) are not cut along the keys: each CTA takes whole items and
 // nothing is joined.  A step of 1, 32 and 128 sequences over 512 bf16 keys (8 x 4 heads), whole against cut:
 // 9.1 / 9.4, 10.7 / 15.7 and 50 / 53 us; over 1024 keys: 12.7 / 11.1, 26.9 / 31.8 and 93 / 91 us, so twice the
-// width where there are many items.
+// width where there are many items (from 64 on: between the 8 and the 256 that were measured).
 constexpr int kWholeKeys = 512, kWholeItems = 64;
 
 // Sequences of at most this many rows (new tokens x query heads of a key/value head) go to the kernel of few

@@ -31,7 +31,8 @@
 // the eight lanes of a load phase on eight different chunks.
 // Measured: 64 sequences of 200 to 8192 e4m3 tokens, 32 over 8 heads (555 MB), 90 to 97 us (5.8 to 6.1 of 6.56
 // TB/s measured copy).  The whole call took 263 us with query rows on the MMA's rows and one CTA an SM, 124 us
-// with two CTAs and cheaper conversions, 102 us with keys on the rows.
+// with two CTAs and cheaper conversions, 102 us with keys on the rows.  (Two column tiles of e4m3 at D = 128 take all
+// 168 registers of two CTAs an SM and spill 22 bytes a thread.)
 #pragma once
 
 #include "exp2_poly.cuh"

@@ -4,9 +4,11 @@
 // relative to, and l = sum w; the row's result is sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  Blocks look at
 // one cut each and join the item it falls into when no earlier cut does.  Few rows have many parts (a long
 // cache over all SMs: 37 of them) and what counts is how many loads are under way: a block of four warps
-// takes one row, a quarter of its parts each, lanes holding the parts' weights.  Many rows have two or three
-// parts: a warp takes two rows.  Where a cut falls was left in the workspace by the CTA whose share begins
-// there: making the plan again in every block cost more than the join (65 us for a batch of prompts).
+// takes one row, a quarter of its parts each, lanes holding the parts' weights.  Many rows mostly have two or three
+// parts: a warp takes two rows, and adds their parts one after the other (up to 148 where one short chunk lies over
+// a long cache: 16 tokens of 8 heads over 131072 keys are 128).  Where a cut falls was left in the workspace by the
+// CTA whose share begins there: making the plan again in every block cost more than the join (65 us for a batch of
+// prompts).
 #pragma once
 
 #include "fa_paged_decode.cuh"

@@ -113,8 +113,8 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
 }
 
 // ------------------------------------------------------------------------------------- the plan
-// Sum of floor((a i + b) / m) over i = 0 .. n - 1 (all non-negative, m > 0): Euclid's steps on the lattice points
-// under the line.  Here n < 2^24, b < 2^31 and a, m are small, so the divisions are of 32 bits.
+// Sum of floor((a i + b) / m) over i = 0 .. n - 1 (all non-negative, m > 0), by the well-known recursion that counts
+// the lattice points under the line with the steps of Euclid's algorithm.  Here n < 2^24, b < 2^31 and a, m are small, so the divisions are of 32 bits.
 FA_HD long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {

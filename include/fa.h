@@ -287,7 +287,9 @@ typedef struct {
  * tokens, scale' = max(scale, s) when the page already holds earlier tokens of
  * the sequence, s otherwise, where s is the smallest power of two >= 2^-100
  * with every new finite |value| <= 448 s; new codes are e4m3(value / scale')
- * (an infinity becomes +-448, a NaN stays one), and when the scale grew the
+ * (an infinity becomes +-448, a NaN stays one; where the caller set a scale
+ * that is no power of two, the quotient is the value times its fp32
+ * reciprocal), and when the scale grew the
  * earlier codes become e4m3(code * scale / scale'), which changes only what
  * falls among e4m3's subnormals.  Slots behind the new tokens keep their bytes.
  *
