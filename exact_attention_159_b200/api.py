@@ -253,8 +253,8 @@ class _Handle:
 class PagedCache(_Handle):
     """A paged key/value cache: k_pages, v_pages [num_pages, Hkv, page_size, d], bf16, or float8_e4m3fn
     with k_scale, v_scale fp32 [num_pages, Hkv] (a held value stands for code * scale; two tensors where
-    tokens are appended, one for both is enough to attend).  page_size 16, 32, 64 or 128; d 64 or 128.  Holds the tensors and describes them to the library; the caller hands
-    out the pages."""
+    tokens are appended, one for both is enough to attend).  page_size 16, 32, 64 or 128; d 64 or 128.
+    Holds the tensors and describes them to the library; the caller hands out the pages."""
 
     def __init__(self, k_pages, v_pages, k_scale=None, v_scale=None):
         if k_pages.dim() != 4:
